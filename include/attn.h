@@ -273,6 +273,150 @@ attn_status_t attn_ring_fwd_host_noalloc(const void* q_h, const void* k_h, const
                                          void* d2h_stream);
 
 /*
+ * Serving operators: what a decoder layer does around its attention when it answers
+ * requests token by token over a paged cache. The pages have no counterpart of these
+ * calls. `lens`, `table`, `slots`, ... are int32 device arrays, so that no call needs the
+ * host to know a request's length; values in them that make no sense (a page or slot
+ * outside the cache, a length beyond the table) never lead to an access out of bounds:
+ * each call states what it does with them.
+ *
+ * The 4-bit cache. Keys and values of one token and key/value head are stored in groups of
+ * 32 values: zero = min (+0 for -0), scale = bf16((max - min) / 15), code =
+ * rint((x - zero) / scale) (ties to the even code; 0 where the scale is 0), value = code * scale + zero; 4 bits a code and a bf16 scale and
+ * zero point a group, 5 bits a value. Inputs must be finite and at most 2^126 in
+ * magnitude; a group with other values reads back as unspecified values, its neighbours
+ * are not affected. The cache is one buffer of
+ *     n_pages * Hkv * page_size / 16 * 20 * d  bytes, 16-byte aligned:
+ * [page][kv head][block of 16 tokens], a block of 20 d bytes holding, in 32-bit words,
+ *     [0, 2d)       key codes, eight to a word, the first in the low bits; word
+ *                   (r, g, t, i) (d = 64: (g, t, r, i)), r < 2, g < 8, t < 4, i < d / 32:
+ *                   token 8r + g, values 32 i + 8 t + (0..7)
+ *     [2d, 4d)      value codes; word (h, g, t, b, a), h < d / 64, g < 8, t < 4, b, a < 2:
+ *                   token 8b + 2t + a, values 64 h + 8 (0..7) + g
+ *     [4d, 4.5d)    key parameters [token][group]: scale in the low 16 bits, zero point high
+ *     [4.5d, 5d)    value parameters, likewise
+ * (the order in which a warp feeds the codes to the tensor core). page_size is a multiple
+ * of 16; slot s of the cache is row s % page_size of page s / page_size; n_pages *
+ * page_size must fit 31 bits. d is 64 or 128. Pages need no initialisation.
+ */
+
+/*
+ * attn_kv_plan - pages and slots for the tokens that a batch of requests is about to add:
+ * request b holds lens[b] tokens in its pages table[b][0 .. ceil(lens[b] / page_size)) and
+ * adds new_lens[b]. The pages it lacks are taken from the free list, in request order:
+ * free_pages[free_head ..). Then
+ *     positions[b][i] = lens[b] + i (modulo 2^32)                     for every i < n_new
+ *     slots[b][i]     = table[b][pos / page_size] * page_size + pos % page_size
+ *                                                  for i < new_lens[b], else -1
+ *     lens_out[b] = lens[b] + new_lens[b],  head_out[0] = free_head[0] + pages taken.
+ * A request is not served (served[b] = 0, its slots -1, lens_out[b] = lens[b], no page
+ * taken) if its length, new_lens[b] < 0 or > n_new make no sense, if it would need more
+ * than `width` pages, or if the free list ends before its last page (requests behind it
+ * that need pages are then not served either). A held page that is negative in the table,
+ * or a slot beyond 31 bits, gives slot -1.
+ *
+ *   table       [B][width], entries of new pages written, all others left as they were
+ *   free_pages  [n_free] page numbers (n_free >= 0; NULL is refused even then)
+ *   slots, positions [B][n_new]; lens_out, served [B]; free_head, head_out [1]
+ * Outputs must not overlap each other or an input: the call may be repeated on the same
+ * inputs with the same result.
+ */
+attn_status_t attn_kv_plan(const int32_t* lens, const int32_t* new_lens, int32_t* table,
+                           const int32_t* free_pages, const int32_t* free_head, int32_t* slots,
+                           int32_t* positions, int32_t* lens_out, int32_t* head_out,
+                           int32_t* served, int B, int n_new, int width, int page_size,
+                           int n_free, void* stream);
+
+/*
+ * attn_qk_norm_rope - norms of queries and keys for each head with the position rotation
+ * in the same pass, from the packed projection to the head-major tensors the attention
+ * calls take. Per query or key head row x: y = x * rsqrt(mean(x^2) + eps) * w, then the
+ * pairs (y[j], y[j + n_freq]) (interleaved = 0) or (y[2j], y[2j + 1]) (interleaved = 1),
+ * j < n_freq, turn by the angle positions[b][i] * inv_freq[j]; values from 2 n_freq on
+ * stay. Value heads are copied. fp32 throughout (angles in fp64), rounded to bf16 once.
+ *
+ *   qkv        device, bf16; row (b, i) at qkv + b * stride_b + i * stride_n (elements,
+ *              multiples of 8) holds Hq query, Hkv key and Hkv value heads of d values;
+ *              16-byte aligned
+ *   wq, wk     device, [d] bf16 (w_fp32 = 0) or fp32 (w_fp32 = 1)
+ *   inv_freq   device, fp32 [n_freq], n_freq a multiple of 8, 2 n_freq <= d
+ *   positions  device, int32 [B][N]
+ *   q, k, v    device, bf16 [B][Hq][N][d], [B][Hkv][N][d], 16-byte aligned (written)
+ */
+attn_status_t attn_qk_norm_rope(const void* qkv, int64_t stride_b, int64_t stride_n,
+                                const void* wq, const void* wk, int w_fp32,
+                                const float* inv_freq, int n_freq, const int32_t* positions,
+                                void* q, void* k, void* v, int B, int N, int Hq, int Hkv, int d,
+                                float eps, int interleaved, void* stream);
+
+/*
+ * attn_kv4_append - tokens into the 4-bit cache: row (b, i) of k and v (bf16
+ * [B][Hkv][N][d], 16-byte aligned) goes to slot slots[b][i]. A slot that is negative or
+ * outside the cache skips its row; everything else in the cache stays as it was. The slots
+ * of one call must differ from each other.
+ */
+attn_status_t attn_kv4_append(const void* k, const void* v, void* cache, const int32_t* slots,
+                              int B, int Hkv, int N, int d, int page_size, int n_pages,
+                              void* stream);
+
+/*
+ * attn_kv4_read - tokens [start[b], start[b] + N) of each request out of the 4-bit cache,
+ * as the bf16 tensors the attention calls take (k, v [B][Hkv][N][d], 16-byte aligned,
+ * written; values rounded to bf16 once). Rows at or past lens[b], rows on a page outside
+ * the cache or the table, and all rows of a request with a negative start are zero.
+ */
+attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32_t* start,
+                            const int32_t* lens, void* k, void* v, int B, int Hkv, int N, int d,
+                            int page_size, int n_pages, int width, void* stream);
+
+/*
+ * attn_kv4_fwd - attention of the newest tokens over the 4-bit cache. Query token i of
+ * request b has position p = q_pos[b] + i (q_pos NULL: lens[b] - Nq + i) and sees the
+ * cached tokens j < lens[b] with j <= p and, when window > 0, (j > p - window or
+ * j < sinks). Returns O and LSE as the other attention calls do (attn_merge joins them
+ * with partials over other keys); rows that see no key give O = 0, LSE = -inf.
+ *
+ *   q        device, bf16 [B][Hq][Nq][d], 16-byte aligned
+ *   table    device, int32 [B][width]; tokens on a page outside the cache are not seen
+ *   lens     device, int32 [B]; a negative length counts as 0, one beyond the table
+ *            (width * page_size) as the table's end
+ *   q_pos    device, int32 [B], or NULL
+ *   o        device, [B][Hq][Nq][d], fp32 (o_bf16 = 0) or bf16 (o_bf16 = 1), 16-byte aligned
+ *   lse      device, fp32 [B][Hq][Nq]
+ *   max_len  the longest request's length as far as the caller knows (0: unknown, the
+ *            table's width counts). It guides how the work is split, never the result's
+ *            definition.
+ *   window   0 (none) or the window's length; sinks >= 0 counts only with a window
+ *   scale    finite, > 0
+ */
+attn_status_t attn_kv4_fwd(const void* q, const void* cache, const int32_t* table,
+                           const int32_t* lens, const int32_t* q_pos, void* o, float* lse,
+                           int o_bf16, int B, int Hq, int Hkv, int Nq, int d, int page_size,
+                           int n_pages, int width, int64_t max_len, int window, int sinks,
+                           float scale, void* stream);
+
+/*
+ * attn_window_fwd - attention with a sliding window and a few first tokens that stay
+ * visible: query row i (position q_off + i) sees key row j (position kv_off + j) when
+ *     kv_off + j <= q_off + i  and  (kv_off + j > q_off + i - window  or  kv_off + j < sinks).
+ * The work grows with window + sinks, not with the sequence. The chunk arguments are those
+ * of attn_fwd_partial, so a prompt can run in pieces (q_off = kv_off + Nkv - Nq for the
+ * newest Nq rows), down to single tokens, and results over disjoint key chunks merge with
+ * attn_merge. Rows that see no key give O = 0, LSE = -inf.
+ *
+ *   q        device, bf16 parent [B][Hq][q_ld][d], rows [0, Nq) of it
+ *   k, v     device, bf16 parents [B][Hkv][kv_ld][d], rows [0, Nkv): rows beyond are never
+ *            read; rows within must be finite
+ *   o        device, dense [B][Hq][Nq][d], fp32 (o_bf16 = 0) or bf16 (o_bf16 = 1)
+ *   lse      device, fp32 [B][Hq][Nq]
+ *   window >= 1, sinks >= 0; scale finite, > 0; d in {64, 128}
+ */
+attn_status_t attn_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                              int o_bf16, int B, int Hq, int Hkv, int64_t Nq, int64_t Nkv,
+                              int64_t q_ld, int64_t kv_ld, int64_t q_off, int64_t kv_off, int d,
+                              int window, int sinks, float scale, void* stream);
+
+/*
  * attn_device_status - synchronise `stream` and report whether any kernel of this
  * library on the current device recorded a device-side failure since the last
  * reset (ATTN_ERR_TIMEOUT: a bounded wait ran out; the kernel then stopped its

@@ -46,6 +46,8 @@ __all__ = [
     "attn_launch_count", "attn_status_string", "attn_version", "lib",
     "attn_debug_wait_timeout", "attn_ring_fwd_host", "RingHostBuffers",
     "attn_ring_fwd_host_noalloc", "ATTN_NOALLOC_SCRATCH_BYTES", "attn_debug_exp2",
+    "kv4_cache", "attn_kv_plan", "attn_qk_norm_rope", "attn_kv4_append", "attn_kv4_read",
+    "attn_kv4_fwd", "attn_window_fwd",
 ]
 
 
@@ -405,3 +407,14 @@ def attn_debug_wait_timeout(limit_cycles: int, stream=None) -> None:
     dev = torch.device("cuda", torch.cuda.current_device())
     _check(lib().attn_debug_wait_timeout(int(limit_cycles), _stream_handle(dev, stream)),
            "attn_debug_wait_timeout")
+
+
+from .serving import (  # noqa: E402  (they use the helpers above)
+    attn_kv4_append,
+    attn_kv4_fwd,
+    attn_kv4_read,
+    attn_kv_plan,
+    attn_qk_norm_rope,
+    attn_window_fwd,
+    kv4_cache,
+)

@@ -62,6 +62,15 @@ SIGNATURES = {
     "attn_ring_fwd_host_noalloc": (_i32, [_c_void_p] * 5 + [_i32, _i32, _i32, _i64, _i32, _i32,
                                                             _i32, _f32, _c_void_p, _c_void_p,
                                                             _c_void_p]),
+    "attn_kv_plan": (_i32, [_c_void_p] * 10 + [_i32] * 5 + [_c_void_p]),
+    "attn_qk_norm_rope": (_i32, [_c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i32, _c_void_p,
+                                 _i32] + [_c_void_p] * 4 + [_i32] * 5 + [_f32, _i32,
+                                                                         _c_void_p]),
+    "attn_kv4_append": (_i32, [_c_void_p] * 4 + [_i32] * 6 + [_c_void_p]),
+    "attn_kv4_read": (_i32, [_c_void_p] * 6 + [_i32] * 7 + [_c_void_p]),
+    "attn_kv4_fwd": (_i32, [_c_void_p] * 7 + [_i32] * 9 + [_i64, _i32, _i32, _f32, _c_void_p]),
+    "attn_window_fwd": (_i32, [_c_void_p] * 5 + [_i32] * 4 + [_i64] * 6 + [_i32, _i32, _i32,
+                                                                           _f32, _c_void_p]),
     "attn_device_status": (_i32, [_c_void_p, _i32]),
     "attn_debug_inject": (_i32, [_i32, _i32]),
     "attn_debug_wait_timeout": (_i32, [_i64, _c_void_p]),

@@ -6,6 +6,7 @@
 #include <vector>
 
 #include "../../include/attn.h"
+#include "api_checks.h"
 #include "attn_internal.h"
 
 namespace {
@@ -13,30 +14,28 @@ namespace {
 int g_inject_status = ATTN_OK;
 int g_inject_count = 0;
 
-// Largest chunk length: TMA row coordinates are 32-bit and a unit reaches 256 rows past
-// its start.
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;
+}  // namespace
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Span {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Span span(const void* p, uint64_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Span{lo, lo + static_cast<uintptr_t>(bytes)};
-}
-
-bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
-
-attn_status_t take_injected() {
+int osx::take_injected() {
   if (g_inject_count > 0) {
     --g_inject_count;
-    return static_cast<attn_status_t>(g_inject_status);
+    return g_inject_status;
   }
   return ATTN_OK;
 }
+
+namespace {
+
+using osx::aligned;
+using osx::overlap;
+using osx::Span;
+using osx::span;
+
+attn_status_t take_injected() { return static_cast<attn_status_t>(osx::take_injected()); }
+
+// Largest chunk length: TMA row coordinates are 32-bit and a unit reaches 256 rows past
+// its start.
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;
 
 attn_status_t check_and_launch(const void* q, const void* k, const void* v, float* o, float* lse,
                                int B, int Hq, int Hkv, int64_t Nq, int64_t Nkv, int64_t q_ld,
@@ -145,7 +144,7 @@ const char* attn_status_string(int status) {
   }
 }
 
-int attn_version(void) { return (1 << 16) | 2; }
+int attn_version(void) { return (1 << 16) | 3; }
 
 attn_status_t attn_fwd(const void* q, const void* k, const void* v, float* o, float* lse, int B,
                        int Hq, int Hkv, int64_t N, int d, int causal, float scale, void* stream) {

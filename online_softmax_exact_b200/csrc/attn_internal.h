@@ -43,4 +43,27 @@ int launch_exp2_probe(const float* x, float* y, long long n, int use_poly, cudaS
 int read_device_status(unsigned* out, int reset);
 uint64_t launch_count();
 
+// Per-device properties of the current device (looked up once per device).
+struct DeviceProps {
+  int num_sms;
+  unsigned* status;  // device address of the status word
+};
+int device_props(DeviceProps* out);
+void count_launch();
+
+// Serving operators (arguments already validated by the ABI layer).
+struct PlanParams;
+struct RopeParams;
+struct Kv4CopyParams;
+struct Kv4FwdParams;
+struct WindowLaunch;
+int launch_window(const WindowLaunch& a, cudaStream_t stream);
+int launch_kv_plan(const PlanParams& p, cudaStream_t stream);
+int launch_qk_norm_rope(const RopeParams& p, int d, int interleaved, cudaStream_t stream);
+int launch_kv4_append(const Kv4CopyParams& p, int d, cudaStream_t stream);
+int launch_kv4_read(const Kv4CopyParams& p, int d, cudaStream_t stream);
+// max_len: the longest request's length as far as the caller knows it (only the split of
+// the work depends on it)
+int launch_kv4_fwd(const Kv4FwdParams& p, int B, int d, long long max_len, cudaStream_t stream);
+
 }  // namespace osx

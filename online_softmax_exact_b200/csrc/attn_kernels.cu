@@ -1,5 +1,5 @@
-// attn_kernels.cu - the library's only device translation unit: kernel instantiations,
-// per-device set-up, and launchers.
+// attn_kernels.cu - device translation unit of the attention forward and merge kernels:
+// instantiations, per-device set-up, and launchers.
 #include <atomic>
 #include <cmath>
 #include <mutex>
@@ -362,6 +362,17 @@ int read_device_status(unsigned* out, int reset) {
   }
   return ATTN_OK;
 }
+
+int device_props(DeviceProps* out) {
+  DeviceInfo* di = nullptr;
+  const int rc = device_info(&di);
+  if (rc != ATTN_OK) return rc;
+  out->num_sms = di->num_sms;
+  out->status = di->status;
+  return ATTN_OK;
+}
+
+void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 uint64_t launch_count() { return g_launches.load(std::memory_order_relaxed); }
 

@@ -1,0 +1,137 @@
+// kv_plan_kernel.cuh - block tables and slot maps of a paged cache, from request lengths.
+//
+// Request b holds len tokens in pages table[b][0 .. held), held = ceil(len / ps), and is
+// about to add `add` tokens: it will need want = ceil((len + add) / ps) pages. Its new
+// pages are entries start_b .. start_b + need_b of the free list, need_b = want - held and
+// start_b = head + the sum of the needs before it: a prefix sum over the requests.
+// Token i then has position len + i and slot table[position / ps] * ps + position % ps.
+//
+// The work is a few integers per token; what bounds it is latency (one launch, two
+// dependent loads) for a decode step and the slot and position stores for large batches.
+// So there is one launch, and every block computes the prefix sums it needs by itself:
+// a block owns kChunk consecutive tokens and scans the requests up to its last one
+// (at most a few thousand integers that all blocks read from L2), instead of waiting for
+// another block or launch. A block never reads a table entry that another writes: pages
+// a request takes now come from the free list, and only pages it held before are read
+// from the table.
+#pragma once
+
+#include <cstdint>
+
+#include "serve_params.h"
+
+namespace osx {
+
+struct PlanRequest {
+  int len, add;        // add: tokens to place (0 when the request is not served)
+  int held;            // pages held before the call
+  int start;           // free-list entry of its first new page
+  bool ok;             // served
+};
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanChunk = 1024;  // tokens a block places
+
+__device__ __forceinline__ int plan_need(const PlanParams& p, int b, int& len, int& add,
+                                         int& held, bool& fits) {
+  len = p.lens[b];
+  add = p.new_lens[b];
+  fits = len >= 0 && add >= 0 && add <= p.n_new;
+  held = 0;
+  if (!fits) return 0;
+  const long long ps = p.page_size;
+  const long long h = (len + ps - 1) / ps, want = ((long long)len + add + ps - 1) / ps;
+  fits = want <= p.width;
+  held = (int)h;
+  return fits ? (int)(want - h) : 0;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams p) {
+  __shared__ PlanRequest req[kPlanChunk + 1];
+  __shared__ long long warp_sum[kPlanThreads / 32];
+  __shared__ long long taken_sum[kPlanThreads / 32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const long long total = (long long)p.B * p.n_new;
+  const long long t0 = (long long)blockIdx.x * kPlanChunk;
+  const long long t1 = t0 + kPlanChunk < total ? t0 + kPlanChunk : total;
+  const int b0 = (int)(t0 / p.n_new), b1 = (int)((t1 - 1) / p.n_new);  // requests of the chunk
+  const int head = *p.free_head;
+
+  long long carry = 0;  // needs of the requests before the current batch of 512
+  long long taken = 0;  // this thread's served needs
+  for (int base = 0; base <= b1; base += kPlanThreads) {
+    const int b = base + threadIdx.x;
+    int len = 0, add = 0, held = 0;
+    bool fits = false;
+    const int need = b < p.B ? plan_need(p, b, len, add, held, fits) : 0;
+    long long incl = need;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long before = carry, all = carry;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      all += warp_sum[w];
+    }
+    incl += before;
+    // served: the request fits its table row, and the free list reaches its last page
+    const bool ok = fits && (need == 0 || (head >= 0 && head + incl <= p.n_free));
+    if (ok) taken += need;
+    if (b >= b0 && b <= b1) {
+      PlanRequest r;
+      r.len = len;
+      r.add = ok ? add : 0;
+      r.held = held;
+      r.start = ok ? (int)(head + incl - need) : 0;
+      r.ok = ok;
+      req[b - b0] = r;
+    }
+    carry = all;
+    __syncthreads();  // warp_sum is rewritten by the next batch; req is complete after it
+  }
+
+  for (long long t = t0 + threadIdx.x; t < t1; t += kPlanThreads) {
+    const int b = (int)(t / p.n_new), i = (int)(t - (long long)b * p.n_new);
+    const PlanRequest r = req[b - b0];
+    const int pos = (int)((unsigned)r.len + (unsigned)i);
+    int slot = -1;
+    if (i < r.add) {
+      const int pg = pos / p.page_size, off = pos - pg * p.page_size;
+      int* entry = p.table + (long long)b * p.width + pg;
+      int page;
+      if (pg >= r.held) {
+        page = p.free_pages[r.start + pg - r.held];
+        // the first new token on the page enters it into the table
+        if (off == 0) *entry = page;
+      } else {
+        page = *entry;
+      }
+      const long long s = (long long)page * p.page_size + off;
+      if (page >= 0 && s <= 0x7fffffffLL) slot = (int)s;
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+    if (i == 0) {
+      p.lens_out[b] = r.len + r.add;
+      p.served[b] = r.ok ? 1 : 0;
+    }
+  }
+
+  if (t1 == total) {  // this block has seen every request: the free list's new head
+#pragma unroll
+    for (int s = 16; s > 0; s /= 2) taken += __shfl_xor_sync(0xffffffffu, taken, s);
+    if (lane == 0) taken_sum[warp] = taken;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      long long sum = 0;
+      for (int w = 0; w < kPlanThreads / 32; ++w) sum += taken_sum[w];
+      *p.head_out = (int)(head + sum);
+    }
+  }
+}
+
+}  // namespace osx

@@ -1,0 +1,202 @@
+// serve_kernels.cu - device translation unit of the serving operators: instantiations and
+// launchers.
+#include <mutex>
+
+#include "../../include/attn.h"
+#include "attn_internal.h"
+#include "attn_window_kernel.cuh"
+#include "kv4_copy_kernels.cuh"
+#include "kv4_fwd_kernel.cuh"
+#include "kv_plan_kernel.cuh"
+#include "qk_norm_rope_kernel.cuh"
+#include "tma_host.h"
+
+namespace osx {
+
+namespace {
+
+int launched() {
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  count_launch();
+  return ATTN_OK;
+}
+
+// Blocks of a one-dimensional grid, or 0 when there are more than a grid can have.
+unsigned grid_1d(long long blocks) {
+  return blocks > 0 && blocks <= 0x7fffffffLL ? static_cast<unsigned>(blocks) : 0u;
+}
+
+// Function attributes of a kernel, set once per device.
+template <auto kKernel>
+int prepare_kernel(uint32_t smem, bool clusters) {
+  constexpr int kMaxDevices = 64;
+  static std::mutex mutex;
+  static bool ready[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return ATTN_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (ready[dev]) return ATTN_OK;
+  if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess)
+    return ATTN_ERR_CUDA;
+  if (clusters && cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                       1) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  ready[dev] = true;
+  return ATTN_OK;
+}
+
+template <int D, int NT>
+int launch_kv4_fwd_dn(Kv4FwdParams p, int B, long long max_len, int num_sms, cudaStream_t stream) {
+  using C = Kv4FwdCfg<D, NT>;
+  p.row_tiles = (p.rows + 8 * NT - 1) / (8 * NT);
+  const long long items = (long long)B * p.Hkv * p.row_tiles;
+  long long keys = max_len;
+  if (p.window && (long long)p.window + p.Nq + p.sinks < keys)
+    keys = (long long)p.window + p.Nq + p.sinks;
+  const long long stages = (keys + 16 * C::kSB - 1) / (16 * C::kSB);
+  // blocks per unit: until the SMs hold two blocks each, while every warp still has a stage
+  int splits = 1;
+  while (splits < 16 && items * splits * 2 <= 2 * num_sms && stages > (long long)splits * C::kWarps)
+    splits *= 2;
+  p.splits = splits;
+  const unsigned grid = grid_1d(items * splits);
+  if (!grid) return ATTN_ERR_UNSUPPORTED;
+  int rc = prepare_kernel<kv4_fwd_kernel<D, NT>>(C::kSmemBytes, true);
+  if (rc != ATTN_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::kWarps * 32);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = splits > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kv4_fwd_kernel<D, NT>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_ERR_CUDA;
+  }
+  return launched();
+}
+
+template <int D>
+int launch_window_d(const WindowLaunch& a, const DeviceProps& dp, cudaStream_t stream) {
+  using C = WindowCfg<D>;
+  CUtensorMap tq, tk, tv;
+  if (!encode_rows_bf16(&tq, a.q, (uint64_t)a.B * a.Hq, a.Nq, a.q_ld, D, 128) ||
+      !encode_rows_bf16(&tk, a.k, (uint64_t)a.B * a.Hkv, a.Nkv, a.kv_ld, D, 128) ||
+      !encode_rows_bf16(&tv, a.v, (uint64_t)a.B * a.Hkv, a.Nkv, a.kv_ld, D, 128))
+    return ATTN_ERR_UNSUPPORTED;
+  WindowParams p;
+  p.status = dp.status;
+  p.o = a.o;
+  p.lse = a.lse;
+  p.o_bf16 = a.o_bf16;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.group = a.Hq / a.Hkv;
+  p.Nq = (int)a.Nq;
+  p.Nkv = (int)a.Nkv;
+  p.rel = a.q_off - a.kv_off;
+  p.window = a.window;
+  const long long s = a.sinks - a.kv_off;
+  p.sinks = (int)(s < 0 ? 0 : (s < a.Nkv ? s : a.Nkv));
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  p.row_blocks = (int)((a.Nq + 255) / 256);
+  const long long units = (long long)a.B * a.Hq * p.row_blocks;
+  if (units > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  p.units = (int)units;
+  const int rc = prepare_kernel<attn_window_kernel<D>>(C::kSmemBytes, false);
+  if (rc != ATTN_OK) return rc;
+  const int grid = units < dp.num_sms ? (int)units : dp.num_sms;
+  attn_window_kernel<D><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
+  return launched();
+}
+
+}  // namespace
+
+int launch_window(const WindowLaunch& a, cudaStream_t stream) {
+  DeviceProps dp;
+  int rc = device_props(&dp);
+  if (rc != ATTN_OK) return rc;
+  return a.d == 128 ? launch_window_d<128>(a, dp, stream) : launch_window_d<64>(a, dp, stream);
+}
+
+int launch_kv_plan(const PlanParams& p, cudaStream_t stream) {
+  DeviceProps dp;
+  int rc = device_props(&dp);
+  if (rc != ATTN_OK) return rc;
+  const unsigned grid = grid_1d(((long long)p.B * p.n_new + kPlanChunk - 1) / kPlanChunk);
+  if (!grid) return ATTN_ERR_UNSUPPORTED;
+  kv_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(p);
+  return launched();
+}
+
+int launch_qk_norm_rope(const RopeParams& p, int d, int interleaved, cudaStream_t stream) {
+  DeviceProps dp;
+  int rc = device_props(&dp);
+  if (rc != ATTN_OK) return rc;
+  const unsigned grid = grid_1d((long long)p.B * p.N);
+  if (!grid) return ATTN_ERR_UNSUPPORTED;
+  if (d == 128) {
+    if (interleaved)
+      qk_norm_rope_kernel<128, true><<<grid, kRopeThreads, 0, stream>>>(p);
+    else
+      qk_norm_rope_kernel<128, false><<<grid, kRopeThreads, 0, stream>>>(p);
+  } else {
+    if (interleaved)
+      qk_norm_rope_kernel<64, true><<<grid, kRopeThreads, 0, stream>>>(p);
+    else
+      qk_norm_rope_kernel<64, false><<<grid, kRopeThreads, 0, stream>>>(p);
+  }
+  return launched();
+}
+
+int launch_kv4_append(const Kv4CopyParams& p, int d, cudaStream_t stream) {
+  DeviceProps dp;
+  int rc = device_props(&dp);
+  if (rc != ATTN_OK) return rc;
+  const unsigned grid =
+      grid_1d(((long long)p.B * p.windows * p.Hkv * 2 + kKv4CopyWarps - 1) / kKv4CopyWarps);
+  if (!grid) return ATTN_ERR_UNSUPPORTED;
+  if (d == 128)
+    kv4_append_kernel<128><<<grid, kKv4CopyWarps * 32, 0, stream>>>(p);
+  else
+    kv4_append_kernel<64><<<grid, kKv4CopyWarps * 32, 0, stream>>>(p);
+  return launched();
+}
+
+int launch_kv4_read(const Kv4CopyParams& p, int d, cudaStream_t stream) {
+  DeviceProps dp;
+  int rc = device_props(&dp);
+  if (rc != ATTN_OK) return rc;
+  const unsigned grid =
+      grid_1d(((long long)p.B * p.windows * p.Hkv * 2 + kKv4CopyWarps - 1) / kKv4CopyWarps);
+  if (!grid) return ATTN_ERR_UNSUPPORTED;
+  if (d == 128)
+    kv4_read_kernel<128><<<grid, kKv4CopyWarps * 32, 0, stream>>>(p);
+  else
+    kv4_read_kernel<64><<<grid, kKv4CopyWarps * 32, 0, stream>>>(p);
+  return launched();
+}
+
+int launch_kv4_fwd(const Kv4FwdParams& params, int B, int d, long long max_len,
+                   cudaStream_t stream) {
+  DeviceProps dp;
+  int rc = device_props(&dp);
+  if (rc != ATTN_OK) return rc;
+  Kv4FwdParams p = params;
+  p.status = dp.status;
+  // 8 query rows a unit, or 16 (the unpacked codes then serve twice the rows)
+  if (d == 128)
+    return p.rows <= 8 ? launch_kv4_fwd_dn<128, 1>(p, B, max_len, dp.num_sms, stream)
+                       : launch_kv4_fwd_dn<128, 2>(p, B, max_len, dp.num_sms, stream);
+  return p.rows <= 8 ? launch_kv4_fwd_dn<64, 1>(p, B, max_len, dp.num_sms, stream)
+                     : launch_kv4_fwd_dn<64, 2>(p, B, max_len, dp.num_sms, stream);
+}
+
+}  // namespace osx

@@ -1,0 +1,94 @@
+// serve_params.h - kernel parameters of the serving operators, shared by the ABI layer,
+// the launchers and the kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+namespace osx {
+
+struct PlanParams {
+  const int* lens;        // [B]
+  const int* new_lens;    // [B]
+  int* table;             // [B][width], entries of new pages written
+  const int* free_pages;  // [n_free]
+  const int* free_head;   // [1]
+  int* slots;             // [B][n_new]
+  int* positions;         // [B][n_new]
+  int* lens_out;          // [B]
+  int* head_out;          // [1]
+  int* served;            // [B]
+  int B, n_new, width, page_size, n_free;
+};
+
+struct RopeParams {
+  const __nv_bfloat16* qkv;  // [B][N][(Hq + 2 Hkv) * d], strides in elements
+  long long stride_b, stride_n;
+  const void* wq;            // [d] bf16 or fp32
+  const void* wk;
+  const float* inv_freq;     // [n_freq]
+  const int* positions;      // [B][N]
+  __nv_bfloat16* q;          // [B][Hq][N][d]
+  __nv_bfloat16* k;          // [B][Hkv][N][d]
+  __nv_bfloat16* v;
+  int B, N, Hq, Hkv, n_freq;
+  int w_fp32;
+  float eps;
+};
+
+struct Kv4CopyParams {
+  const __nv_bfloat16* k;   // append: [B][Hkv][N][d]
+  const __nv_bfloat16* v;
+  __nv_bfloat16* k_out;     // read: [B][Hkv][N][d]
+  __nv_bfloat16* v_out;
+  uint32_t* cache;
+  const int* slots;         // append: [B][N]
+  const int* table;         // read: [B][width]
+  const int* start;         // read: [B]
+  const int* lens;          // read: [B]
+  int B, N, Hkv, page_size, n_pages, width, windows;
+};
+
+struct Kv4FwdParams {
+  const __nv_bfloat16* q;   // [B][Hq][Nq][D]
+  const uint32_t* cache;
+  const int* table;         // [B][width]
+  const int* lens;          // [B]
+  const int* q_pos;         // [B] position of the first query token, or null: lens - Nq
+  void* o;                  // [B][Hq][Nq][D] fp32 or bf16
+  float* lse;               // [B][Hq][Nq]
+  unsigned* status;
+  int o_bf16;
+  int Hkv, Nq, rows, row_tiles;   // rows = group * Nq
+  int blocks_per_page, n_pages, width;
+  int window, sinks, splits;
+  float scale_log2;
+};
+
+struct WindowLaunch {
+  const void* q;  // bf16 [B][Hq][q_ld][d], rows [0, Nq)
+  const void* k;  // bf16 [B][Hkv][kv_ld][d], rows [0, Nkv)
+  const void* v;
+  void* o;        // [B][Hq][Nq][d] fp32 or bf16
+  float* lse;     // [B][Hq][Nq]
+  int o_bf16, B, Hq, Hkv;
+  long long Nq, Nkv, q_ld, kv_ld, q_off, kv_off;
+  int d, window;
+  long long sinks;
+  float scale;
+};
+
+struct WindowParams {
+  void* o;
+  float* lse;
+  unsigned* status;
+  int o_bf16, Hq, Hkv, group;
+  int Nq, Nkv;
+  long long rel;     // position of query row 0 less that of key row 0
+  int window, sinks; // sinks: key rows [0, sinks) of this chunk stay visible
+  int row_blocks, units;
+  float scale_log2;
+};
+
+}  // namespace osx
