@@ -388,12 +388,21 @@ attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32
  *            definition.
  *   window   0 (none) or the window's length; sinks >= 0 counts only with a window
  *   scale    finite, > 0
+ *   workspace  device, 16-byte aligned, at least attn_kv4_fwd_workspace(...) bytes (about
+ *            5 MB); its contents on entry do not matter, and nothing in it is kept. Calls
+ *            whose work may overlap on the GPU need workspaces of their own.
+ * Query rows may be of any size below 2^112, cached values up to 2^24 in magnitude. The
+ * same inputs give the same bits.
  */
 attn_status_t attn_kv4_fwd(const void* q, const void* cache, const int32_t* table,
                            const int32_t* lens, const int32_t* q_pos, void* o, float* lse,
                            int o_bf16, int B, int Hq, int Hkv, int Nq, int d, int page_size,
                            int n_pages, int width, int64_t max_len, int window, int sinks,
-                           float scale, void* stream);
+                           float scale, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+
+/* Bytes of workspace that attn_kv4_fwd needs for these sizes (0: sizes it would refuse). */
+int64_t attn_kv4_fwd_workspace(int B, int Hq, int Hkv, int Nq, int d);
 
 /*
  * attn_window_fwd - attention with a sliding window and a few first tokens that stay

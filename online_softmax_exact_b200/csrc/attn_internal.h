@@ -62,8 +62,15 @@ int launch_kv_plan(const PlanParams& p, cudaStream_t stream);
 int launch_qk_norm_rope(const RopeParams& p, int d, int interleaved, cudaStream_t stream);
 int launch_kv4_append(const Kv4CopyParams& p, int d, cudaStream_t stream);
 int launch_kv4_read(const Kv4CopyParams& p, int d, cudaStream_t stream);
-// max_len: the longest request's length as far as the caller knows it (only the split of
-// the work depends on it)
-int launch_kv4_fwd(const Kv4FwdParams& p, int B, int d, long long max_len, cudaStream_t stream);
+// Workspace of launch_kv4_fwd: byte offsets of its parts, and its size. The prefix sums
+// are at offset 0.
+struct Kv4Workspace {
+  long long ml, o, bytes;
+};
+constexpr int kKv4MaxBlocks = 160;  // blocks of the attention launch at most
+Kv4Workspace kv4_workspace(int B, int Hkv, int rows, int d);
+// max_len: the longest request's length as far as the caller knows it (only the number of
+// blocks depends on it)
+int launch_kv4_fwd(const Kv4FwdParams& p, int d, long long max_len, cudaStream_t stream);
 
 }  // namespace osx

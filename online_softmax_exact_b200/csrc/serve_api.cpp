@@ -184,18 +184,25 @@ attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32
   return static_cast<attn_status_t>(osx::launch_kv4_read(p, d, static_cast<cudaStream_t>(stream)));
 }
 
+int64_t attn_kv4_fwd_workspace(int B, int Hq, int Hkv, int Nq, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Nq < 1 || (d != 64 && d != 128) ||
+      too_many(B, Hq, 1 << 30) || too_many(Hq, Nq, 1 << 30))
+    return 0;
+  return osx::kv4_workspace(B, Hkv, Hq / Hkv * Nq, d).bytes;
+}
+
 attn_status_t attn_kv4_fwd(const void* q, const void* cache, const int32_t* table,
                            const int32_t* lens, const int32_t* q_pos, void* o, float* lse,
                            int o_bf16, int B, int Hq, int Hkv, int Nq, int d, int page_size,
                            int n_pages, int width, int64_t max_len, int window, int sinks,
-                           float scale, void* stream) {
-  if (!q || !table || !lens || !o || !lse) return ATTN_ERR_INVALID_ARG;
+                           float scale, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!q || !table || !lens || !o || !lse || !workspace) return ATTN_ERR_INVALID_ARG;
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Nq < 1 || width < 1 || max_len < 0)
     return ATTN_ERR_INVALID_ARG;
   if ((o_bf16 != 0 && o_bf16 != 1) || window < 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(table, 4) ||
-      !aligned(lens, 4) || !aligned(q_pos, 4))
+      !aligned(lens, 4) || !aligned(q_pos, 4) || !aligned(workspace, 16))
     return ATTN_ERR_INVALID_ARG;
   const attn_status_t st = check_cache(cache, Hkv, d, page_size, n_pages);
   if (st != ATTN_OK) return st;
@@ -206,8 +213,11 @@ attn_status_t attn_kv4_fwd(const void* q, const void* cache, const int32_t* tabl
   const Span in[5] = {span(q, rows * d * 2), span(cache, cache_bytes(Hkv, d, page_size, n_pages)),
                       span(table, (uint64_t)B * width * 4), span(lens, (uint64_t)B * 4),
                       span(q_pos ? q_pos : lens, (uint64_t)B * 4)};
-  const Span out[2] = {span(o, rows * d * (o_bf16 ? 2 : 4)), span(lse, rows * 4)};
-  if (!apart(out, 2, in, 5)) return ATTN_ERR_INVALID_ARG;
+  const osx::Kv4Workspace ws = osx::kv4_workspace(B, Hkv, Hq / Hkv * Nq, d);
+  if (workspace_bytes < ws.bytes) return ATTN_ERR_INVALID_ARG;
+  const Span out[3] = {span(o, rows * d * (o_bf16 ? 2 : 4)), span(lse, rows * 4),
+                       span(workspace, (uint64_t)ws.bytes)};
+  if (!apart(out, 3, in, 5)) return ATTN_ERR_INVALID_ARG;
   const int inj = osx::take_injected();
   if (inj != ATTN_OK) return static_cast<attn_status_t>(inj);
   const int64_t room = (int64_t)width * page_size;
@@ -220,17 +230,24 @@ attn_status_t attn_kv4_fwd(const void* q, const void* cache, const int32_t* tabl
   p.o = o;
   p.lse = lse;
   p.o_bf16 = o_bf16;
+  p.ws_prefix = static_cast<long long*>(workspace);
+  p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.ml);
+  p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.o);
+  p.B = B;
   p.Hkv = Hkv;
   p.Nq = Nq;
   p.rows = Hq / Hkv * Nq;
   p.blocks_per_page = page_size / 16;
+  p.page_magic = p.blocks_per_page == 1
+                     ? 0xffffffffu
+                     : static_cast<uint32_t>((uint64_t(1) << 32) / p.blocks_per_page);
   p.n_pages = n_pages;
   p.width = width;
   p.window = window;
   p.sinks = sinks;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   return static_cast<attn_status_t>(
-      osx::launch_kv4_fwd(p, B, d, max_len > 0 && max_len < room ? max_len : room,
+      osx::launch_kv4_fwd(p, d, max_len > 0 && max_len < room ? max_len : room,
                           static_cast<cudaStream_t>(stream)));
 }
 

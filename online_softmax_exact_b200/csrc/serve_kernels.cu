@@ -46,41 +46,64 @@ int prepare_kernel(uint32_t smem, bool clusters) {
   return ATTN_OK;
 }
 
-template <int D, int NT>
-int launch_kv4_fwd_dn(Kv4FwdParams p, int B, long long max_len, int num_sms, cudaStream_t stream) {
-  using C = Kv4FwdCfg<D, NT>;
-  p.row_tiles = (p.rows + 8 * NT - 1) / (8 * NT);
-  const long long items = (long long)B * p.Hkv * p.row_tiles;
-  long long keys = max_len;
-  if (p.window && (long long)p.window + p.Nq + p.sinks < keys)
-    keys = (long long)p.window + p.Nq + p.sinks;
-  const long long stages = (keys + 16 * C::kSB - 1) / (16 * C::kSB);
-  // blocks per unit: until the SMs hold two blocks each, while every warp still has a stage
-  int splits = 1;
-  while (splits < 16 && items * splits * 2 <= 2 * num_sms && stages > (long long)splits * C::kWarps)
-    splits *= 2;
-  p.splits = splits;
-  const unsigned grid = grid_1d(items * splits);
-  if (!grid) return ATTN_ERR_UNSUPPORTED;
-  int rc = prepare_kernel<kv4_fwd_kernel<D, NT>>(C::kSmemBytes, true);
-  if (rc != ATTN_OK) return rc;
+// A launch whose blocks may start before the launch before it in the stream has ended (they
+// wait for it in the kernel): its launch latency and set-up lie beside that one's end.
+template <class... A>
+int launch_dependent(void (*kernel)(A...), unsigned grid, unsigned threads, cudaStream_t stream,
+                     A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(C::kWarps * 32);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = splits;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, kv4_fwd_kernel<D, NT>, p) != cudaSuccess) {
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_CUDA;
   }
   return launched();
+}
+
+template <int D, int NT>
+int launch_kv4_fwd_dn(Kv4FwdParams p, long long max_len, int num_sms, cudaStream_t stream) {
+  using C = Kv4FwdCfg<D, NT>;
+  p.row_tiles = (p.rows + C::kRows - 1) / C::kRows;
+  const long long items = (long long)p.B * p.Hkv * p.row_tiles;
+  const unsigned join_grid = grid_1d(items * C::kRows * (D / 64));
+  if (!join_grid) return ATTN_ERR_UNSUPPORTED;
+  // one block per SM, or fewer where there cannot be a stage for each of their warps
+  long long keys = max_len;
+  if (p.window && (long long)p.window + p.Nq + p.sinks < keys)
+    keys = (long long)p.window + p.Nq + p.sinks;
+  const long long stages = items * (keys / (16 * C::kSB) + 2);
+  int grid = num_sms < kKv4MaxBlocks ? num_sms : kKv4MaxBlocks;
+  if (stages < grid) grid = (int)stages;
+  const int rc = prepare_kernel<kv4_fwd_kernel<D, NT>>(C::kSmemBytes, false);
+  if (rc != ATTN_OK) return rc;
+  kv4_fwd_kernel<D, NT><<<grid, C::kWarps * 32, C::kSmemBytes, stream>>>(p);
+  const int st = launched();
+  if (st != ATTN_OK) return st;
+  // a unit has about warps / units partials
+  if (items * 16 >= grid * C::kWarps)
+    return launch_dependent(kv4_join_kernel<D, C::kRows, 128>, join_grid, 128, stream, p,
+                            grid * C::kWarps);
+  return launch_dependent(kv4_join_kernel<D, C::kRows, 512>, join_grid, 512, stream, p,
+                          grid * C::kWarps);
+}
+
+template <int D, int NT>
+Kv4Workspace kv4_workspace_dn(int B, int Hkv, int rows) {
+  using C = Kv4FwdCfg<D, NT>;
+  const long long items = (long long)B * Hkv * ((rows + C::kRows - 1) / C::kRows);
+  const long long slots = (long long)kKv4MaxBlocks * C::kWarps + items;
+  Kv4Workspace w;
+  w.ml = ((long long)(B + 1) * 8 + 255) / 256 * 256;
+  w.o = w.ml + (slots * C::kRows * 2 * 4 + 255) / 256 * 256;
+  w.bytes = w.o + slots * C::kRows * D * 4;
+  return w;
 }
 
 template <int D>
@@ -184,19 +207,24 @@ int launch_kv4_read(const Kv4CopyParams& p, int d, cudaStream_t stream) {
   return launched();
 }
 
-int launch_kv4_fwd(const Kv4FwdParams& params, int B, int d, long long max_len,
-                   cudaStream_t stream) {
+// 4 query rows a unit, or 8 (the unpacked codes then serve twice the rows)
+Kv4Workspace kv4_workspace(int B, int Hkv, int rows, int d) {
+  if (d == 128)
+    return rows <= 4 ? kv4_workspace_dn<128, 1>(B, Hkv, rows) : kv4_workspace_dn<128, 2>(B, Hkv, rows);
+  return rows <= 4 ? kv4_workspace_dn<64, 1>(B, Hkv, rows) : kv4_workspace_dn<64, 2>(B, Hkv, rows);
+}
+
+int launch_kv4_fwd(const Kv4FwdParams& params, int d, long long max_len, cudaStream_t stream) {
   DeviceProps dp;
   int rc = device_props(&dp);
   if (rc != ATTN_OK) return rc;
   Kv4FwdParams p = params;
   p.status = dp.status;
-  // 8 query rows a unit, or 16 (the unpacked codes then serve twice the rows)
   if (d == 128)
-    return p.rows <= 8 ? launch_kv4_fwd_dn<128, 1>(p, B, max_len, dp.num_sms, stream)
-                       : launch_kv4_fwd_dn<128, 2>(p, B, max_len, dp.num_sms, stream);
-  return p.rows <= 8 ? launch_kv4_fwd_dn<64, 1>(p, B, max_len, dp.num_sms, stream)
-                     : launch_kv4_fwd_dn<64, 2>(p, B, max_len, dp.num_sms, stream);
+    return p.rows <= 4 ? launch_kv4_fwd_dn<128, 1>(p, max_len, dp.num_sms, stream)
+                       : launch_kv4_fwd_dn<128, 2>(p, max_len, dp.num_sms, stream);
+  return p.rows <= 4 ? launch_kv4_fwd_dn<64, 1>(p, max_len, dp.num_sms, stream)
+                     : launch_kv4_fwd_dn<64, 2>(p, max_len, dp.num_sms, stream);
 }
 
 }  // namespace osx

@@ -60,9 +60,13 @@ struct Kv4FwdParams {
   float* lse;               // [B][Hq][Nq]
   unsigned* status;
   int o_bf16;
-  int Hkv, Nq, rows, row_tiles;   // rows = group * Nq
+  float* ws_o;              // partials by slot: rows, (base, denominator) pairs
+  float* ws_ml;
+  long long* ws_prefix;     // [B + 1] stages before each request
+  int B, Hkv, Nq, rows, row_tiles;   // rows = group * Nq
   int blocks_per_page, n_pages, width;
-  int window, sinks, splits;
+  uint32_t page_magic;      // floor(2^32 / blocks_per_page), 2^32 - 1 for one
+  int window, sinks;
   float scale_log2;
 };
 

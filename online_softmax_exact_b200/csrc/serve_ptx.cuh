@@ -1,5 +1,5 @@
-// serve_ptx.cuh - inline-PTX wrappers of the decode kernels: untiled bulk copies, warp
-// matrix products, cluster barriers and distributed shared memory.
+// serve_ptx.cuh - inline-PTX wrappers of the serving kernels: untiled bulk copies, warp
+// matrix products, dependent launches.
 #pragma once
 
 #include <cstdint>
@@ -31,6 +31,24 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with D = A * B.
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// D (16 x 8) += A (16 x 8, rows) * B (8 x 8, columns): a0 (row g, k 2t 2t+1), a1 (row g+8);
+// b0 (k 2t 2t+1, column g).
+__device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+
 // 8 x 8 transposition of 16-bit values across the warp (one register per lane).
 __device__ __forceinline__ uint32_t transpose_b16(uint32_t x) {
   uint32_t y;
@@ -38,24 +56,14 @@ __device__ __forceinline__ uint32_t transpose_b16(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
+// Programmatic dependent launch: wait until the launch before this one in the stream has
+// ended and its writes are visible (at once in an ordinary launch); and, in that one, let
+// the next launch's blocks start when SMs have room for them.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
-
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
-}
-
-// A float of another block of the cluster: `addr` is its address in this block's window.
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void grid_dependents_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 __device__ __forceinline__ float lg2_approx(float x) {

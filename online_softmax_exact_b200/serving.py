@@ -16,8 +16,6 @@ requests reads::
 
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _check, _stream_handle, lib
@@ -63,18 +61,31 @@ def _out(t, shape, dtype, device: torch.device, name: str) -> torch.Tensor:
     return t
 
 
+def _raw_stream(device: torch.device, stream, tensors) -> int:
+    """The handle of ``stream``, or of the device's current stream. Tensors used on a stream
+    other than the current one are recorded there, so that their memory is not reused too
+    early."""
+    here = torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None:
+        return here
+    handle = _stream_handle(device, stream)
+    if handle != here and isinstance(stream, torch.cuda.Stream):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    return handle
+
+
 def _launch(entry: str, device: torch.device, stream, tensors, *args) -> None:
-    """Call the entry point with ``device`` current. Tensors used on a stream other than
-    the current one are recorded there, so that their memory is not reused too early."""
-    here = device.index == torch.cuda.current_device()
-    with contextlib.nullcontext() if here else torch.cuda.device(device):
-        handle = _stream_handle(device, stream)
-        if isinstance(stream, torch.cuda.Stream) and stream != torch.cuda.current_stream(device):
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
+    """Call the entry point on the stream with ``device`` current."""
+    handle = _raw_stream(device, stream, tensors)
+    if device.index == torch.cuda.current_device():
         st = getattr(lib(), entry)(*args, handle)
-    _check(st, entry)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(lib(), entry)(*args, handle)
+    if st:
+        _check(st, entry)
 
 
 def kv4_cache(n_pages: int, n_kv_heads: int, d: int, *, page_size: int = 64,
@@ -234,12 +245,15 @@ def attn_kv4_fwd(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens
     o = _out(o, (B, Hq, Nq, d), _BF16 if bf16 else _F32, dev, "o")
     lse = _out(lse, (B, Hq, Nq), _F32, dev, "lse")
     size = torch.Size((B,))
-    _launch("attn_kv4_fwd", dev, stream, (q, cache, table, lens, q_pos, o, lse),
+    n_ws = lib().attn_kv4_fwd_workspace(B, Hq, Hkv, Nq, d)
+    ws = torch.empty(n_ws, dtype=_U8, device=dev)
+    _launch("attn_kv4_fwd", dev, stream, (q, cache, table, lens, q_pos, o, lse, ws),
             _arg(q, _BF16, q.shape, "q", dev), c_p, _arg(table, _I32, table.shape, "table", dev),
             _arg(lens, _I32, size, "lens", dev),
             None if q_pos is None else _arg(q_pos, _I32, size, "q_pos", dev), o.data_ptr(),
             lse.data_ptr(), bf16, B, Hq, Hkv, Nq, d, page, n_pages, table.shape[1], int(max_len),
-            int(window), int(sinks), float(d ** -0.5 if scale is None else scale))
+            int(window), int(sinks), float(d ** -0.5 if scale is None else scale),
+            ws.data_ptr(), n_ws)
     return o, lse
 
 

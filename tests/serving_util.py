@@ -170,20 +170,23 @@ def visible(pos, key, window, sinks):
     return see
 
 
-def attention(q, k, v, see, scale, kmag=None, vmag=None, o_bf16=False):
+def attention(q, k, v, see, scale, kmag=None, vmag=None, vfull=None, wround=HALF_BF16,
+              o_bf16=False):
     """One head by the definition: q [n, d], k, v [m, d], see [n, m] ->
     (o, lse, bound on |dO|, bound on |dLSE|).
 
     kmag [m, d]: the size of the terms whose sum a key value is in the kernel (default |k|);
-    vmag [m, d]: the part of a value whose weight is rounded to bf16 (default |v|).
+    vmag [m, d]: the part of a value whose weight is rounded for the matrix unit (default
+    |v|), by wround (bf16: 2^-8); vfull [m, d]: the size of all its terms (default |v|).
     Scores: fp32 sums of d products (each addition off by at most 2^-23 of the terms, since a
     matrix unit may cut rather than round), so a score is off by at most
     es = (d + 4) 2^-23 scale sum |q| kmag, a weight by a factor e^(2 es) (its own score and
-    the denominator) plus the exponential's 2^-21; the matrix operand's rounding adds
-    2^-8 of p vmag; O's own rounding 2^-8 of |O| (bf16) or 2^-22 (fp32, with the sums)."""
+    the denominator) plus the exponential's 2^-21; O's own rounding is 2^-8 of |O| (bf16) or
+    2^-22 (fp32, with the sums)."""
     n, d = q.shape
     kmag = np.abs(k) if kmag is None else kmag
     vmag = np.abs(v) if vmag is None else vmag
+    vfull = np.abs(v) if vfull is None else vfull
     s = np.where(see, q @ k.T * scale, -np.inf)
     es = np.where(see, (np.abs(q) @ kmag.T) * scale * (d + 4) * 2.0 ** -23, 0).max(-1, initial=0)
     m = s.max(-1, initial=-np.inf)
@@ -195,7 +198,7 @@ def attention(q, k, v, see, scale, kmag=None, vmag=None, o_bf16=False):
     p = p / np.where(l > 0, l, 1)[:, None]
     o = p @ v
     rel = np.expm1(2 * es) + 2.0 ** -20
-    bo = rel[:, None] * (p @ (np.abs(v) + vmag)) + HALF_BF16 * (p @ vmag) * (1 + rel[:, None])
+    bo = rel[:, None] * (p @ vfull) + wround * (p @ vmag) * (1 + rel[:, None])
     bo += (HALF_BF16 if o_bf16 else 2.0 ** -22) * (np.abs(o) + bo) + 1e-30
     bl = es + 2.0 ** -20 + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0))
     return o, lse, bo, bl

@@ -183,15 +183,15 @@ def fwd_case(osx, seed, B, Hq, Hkv, Nq, d, page, lens, window=0, sinks=0, q_pos=
             kc, ks, kz = take(kp)
             vc, vs, vz = take(vp)
             kf, vf = su.values(kc, ks, kz), su.values(vc, vs, vz)
-            # the kernel sums scale (128 + c) and zero - 128 scale apart, and rounds the
-            # weight of scale (c - 8)
-            kmag = su.values(kc + 128, ks, np.abs(kz - 128 * ks))
-            vmag = np.abs(su.values(vc - 8, vs, 0 * vz))
+            # the kernel sums scale * c and zero apart; the weight of scale * c enters as
+            # two bf16 numbers, each cut (not rounded) to 8 bits: what is left after the
+            # first is below 2^-7 of it, what is left after the second below 2^-7 of that
+            kmag, vmag = su.values(kc, ks, np.abs(kz)), su.values(vc, vs, 0 * vz)
+            vfull = su.values(vc, vs, np.abs(vz))
             for x in range(Hq // Hkv):
                 r = h * (Hq // Hkv) + x
                 ref = su.attention(qn[b, r], kf, vf, see, np.float64(np.float32(scale)), kmag,
-                                   vmag + np.abs(su.values(0 * vc, vs, vz + 8 * vs)) * 2.0 ** -12,
-                                   o_bf16=o_dtype == torch.bfloat16)
+                                   vmag, vfull, 2.0 ** -14, o_dtype == torch.bfloat16)
                 su.check(on[b, r], ln[b, r], ref, f"request {b} head {r}")
     return o, lse
 
@@ -284,5 +284,5 @@ def test_fwd_is_deterministic_and_merges(osx):
     a = osx.attn_kv4_fwd(q, cg, table[:, :17].contiguous(), i32([272]))
     b = osx.attn_kv4_fwd(q, cg, table[:, 17:].contiguous(), i32([368]))
     om, lm = osx.attn_merge([a[0], b[0]], [a[1], b[1]])
-    # weights rounded against other bases: 2^-8 each way of values up to 5 in size
-    assert (om - o).abs().max() <= 2 * 5 * su.HALF_BF16 and (lm - lse).abs().max() <= 1e-4
+    # weights rounded against other bases: 2^-14 each way of scale * c, up to 0.4 * 15
+    assert (om - o).abs().max() <= 2 * 6 * 2.0 ** -14 and (lm - lse).abs().max() <= 1e-4

@@ -48,7 +48,7 @@ READ = dict(cache=G, table=2 * G, start=3 * G, lens=4 * G, k=5 * G, v=6 * G, B=2
             page=16, n_pages=9, width=4, stream=None)
 KV4 = dict(q=G, cache=2 * G, table=3 * G, lens=4 * G, q_pos=None, o=5 * G, lse=6 * G, o_bf16=0, B=2,
            Hq=4, Hkv=2, Nq=1, d=64, page=16, n_pages=9, width=4, max_len=0, window=0, sinks=0,
-           scale=0.125, stream=None)
+           scale=0.125, ws=8 * G, ws_bytes=1 << 24, stream=None)
 WIN = dict(q=G, k=2 * G, v=3 * G, o=4 * G, lse=5 * G, o_bf16=0, B=2, Hq=4, Hkv=2, Nq=8, Nkv=16,
            q_ld=8, kv_ld=16, q_off=8, kv_off=0, d=64, window=4, sinks=1, scale=0.125, stream=None)
 
@@ -74,7 +74,8 @@ INVALID = {
         dict(table=2 * G + 1), dict(B=0), dict(N=0), dict(width=0), dict(page=8), dict(n_pages=0),
         dict(k=6 * G), dict(k=G), dict(v=2 * G)]),
     "attn_kv4_fwd": (KV4, [
-        *({k: None} for k in ("q", "cache", "table", "lens", "o", "lse")), dict(q=G + 8),
+        *({k: None} for k in ("q", "cache", "table", "lens", "o", "lse", "ws")), dict(q=G + 8),
+        dict(ws=8 * G + 8), dict(ws_bytes=1 << 20), dict(ws=G - 4096), dict(ws=5 * G),
         dict(o=5 * G + 4), dict(q_pos=7 * G + 2), dict(B=0), dict(Hq=3), dict(Hkv=0), dict(Nq=0),
         dict(width=0), dict(max_len=-1), dict(o_bf16=2), dict(window=-1), dict(sinks=-1),
         dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
@@ -119,6 +120,16 @@ def test_unsupported_arguments(lib, entry):
         # addresses far enough apart for the larger sizes
         wide = {k: v << 8 for k, v in defaults.items() if isinstance(v, int) and v >= G}
         assert call(getattr(lib, entry), {**defaults, **wide}, **kw) == unsupported, kw
+
+
+def test_kv4_workspace(lib):
+    size = lib.attn_kv4_fwd_workspace
+    for bad in ((0, 4, 2, 1, 64), (1, 3, 2, 1, 64), (1, 4, 2, 0, 64), (1, 4, 2, 1, 96)):
+        assert size(*bad) == 0
+    need = size(2, 4, 2, 1, 64)
+    invalid, _ = statuses()
+    assert call(lib.attn_kv4_fwd, KV4, ws_bytes=need - 1) == invalid
+    assert 0 < need < size(2, 4, 2, 1, 128) < size(200, 32, 8, 1, 128) < 1 << 25
 
 
 @pytest.mark.parametrize("entry", sorted(DEFAULTS))
