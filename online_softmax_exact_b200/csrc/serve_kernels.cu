@@ -163,19 +163,16 @@ int launch_qk_norm_rope(const RopeParams& p, int d, int interleaved, cudaStream_
   DeviceProps dp;
   int rc = device_props(&dp);
   if (rc != ATTN_OK) return rc;
-  const unsigned grid = grid_1d((long long)p.B * p.N);
-  if (!grid) return ATTN_ERR_UNSUPPORTED;
-  if (d == 128) {
-    if (interleaved)
-      qk_norm_rope_kernel<128, true><<<grid, kRopeThreads, 0, stream>>>(p);
-    else
-      qk_norm_rope_kernel<128, false><<<grid, kRopeThreads, 0, stream>>>(p);
-  } else {
-    if (interleaved)
-      qk_norm_rope_kernel<64, true><<<grid, kRopeThreads, 0, stream>>>(p);
-    else
-      qk_norm_rope_kernel<64, false><<<grid, kRopeThreads, 0, stream>>>(p);
-  }
+  // a warp per token, or up to eight where that would leave warps idle (four blocks an SM)
+  constexpr int kWarps = kRopeThreads / 32;
+  const long long tokens = (long long)p.B * p.N, warps = 4ll * dp.num_sms * kWarps;
+  int split = 1;
+  while (split < kWarps && tokens * split * 2 <= warps) split *= 2;
+  const long long blocks = (tokens * split + kWarps - 1) / kWarps, most = 4ll * dp.num_sms;
+  const unsigned grid = grid_1d(blocks < most ? blocks : most);
+  auto* kernel = d == 128 ? (interleaved ? qk_norm_rope_kernel<128, true> : qk_norm_rope_kernel<128, false>)
+                          : (interleaved ? qk_norm_rope_kernel<64, true> : qk_norm_rope_kernel<64, false>);
+  kernel<<<grid, kRopeThreads, 0, stream>>>(p, split);
   return launched();
 }
 

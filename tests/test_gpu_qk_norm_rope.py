@@ -38,7 +38,7 @@ def check(osx, B, N, Hq, Hkv, d, r, interleaved, w_dtype=torch.bfloat16, far=0, 
                                 interleaved)
         # one rounding to bf16, and fp32 arithmetic: the norm (d terms, each within 2^-24,
         # under a root: (d / 2 + 4) 2^-24 of the value) and the rotation (angle within
-        # 2^-22 after its reduction to [-pi, pi], sine and cosine within 2^-22)
+        # 2^-22 after its reduction to [-pi, pi], sine and cosine within 2^-21.1: 2^-20)
         err = mag * ((d / 2 + 4) * 2.0 ** -24 + 2.0 ** -20)
         bound = su.HALF_BF16 * (np.abs(ref) + err) + err + 1e-38
         assert (np.abs(su.to_np(got) - ref) <= bound).all()
