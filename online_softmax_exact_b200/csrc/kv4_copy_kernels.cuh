@@ -37,15 +37,6 @@ __device__ __forceinline__ bool kv4_copy_item(const Kv4CopyParams& p, int& b, in
   return true;
 }
 
-// The group's parameter word; lo becomes the zero point (a minimum of -0 is stored as +0:
-// which of the two a minimum of both is, is not defined).
-__device__ __forceinline__ uint32_t group_params(float& lo, float hi, float& scale) {
-  lo += 0.f;
-  const __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(hi - lo, 15.f));
-  scale = __bfloat162float(s);
-  return (uint32_t)__bfloat16_as_ushort(s) | (__float_as_uint(lo) & 0xffff0000u);
-}
-
 template <int D>
 __global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_append_kernel(const Kv4CopyParams p) {
   using L = Kv4<D>;
@@ -94,22 +85,9 @@ __global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_append_kernel(const Kv
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int i = 0; i < L::kGroups; ++i) {
-        float f[8];
-        unpack8(raw[r][i], f);
-        float lo = f[0], hi = f[0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) {
-          lo = fminf(lo, f[e]);
-          hi = fmaxf(hi, f[e]);
-        }
-#pragma unroll
-        for (int s = 1; s < 4; s *= 2) {
-          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, s));
-          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, s));
-        }
-        float scale;
-        par[r][i] = group_params(lo, hi, scale);
-        word[r][i] = quant8(f, lo, scale);
+        float lo, range;
+        group_range<1>(raw[r][i], &lo, &range);
+        word[r][i] = quant8(raw[r][i], lo, range, &par[r][i]);
       }
     if (whole) {
       uint32_t* blk = block_of(base);
@@ -122,16 +100,22 @@ __global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_append_kernel(const Kv
         *reinterpret_cast<uint4*>(blk + lane * 4) =
             make_uint4(word[0][0], word[0][1], word[1][0], word[1][1]);
       }
-    }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if (slot[r] < 0) continue;
-      uint32_t* blk = block_of(slot[r]);
-      const int row = slot[r] % 16;  // page_size is a multiple of 16
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int i = 0; i < L::kGroups; ++i) {
-        if (!whole) blk[L::k_word(row, t, i)] = word[r][i];
-        if (t == i) blk[L::kKParams + row * L::kGroups + i] = par[r][i];
+        for (int i = 0; i < L::kGroups; ++i)
+          if (t == i) blk[L::kKParams + (8 * r + g) * L::kGroups + i] = par[r][i];
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (slot[r] < 0) continue;
+        uint32_t* blk = block_of(slot[r]);
+        const int row = slot[r] % 16;  // page_size is a multiple of 16
+#pragma unroll
+        for (int i = 0; i < L::kGroups; ++i) {
+          blk[L::k_word(row, t, i)] = word[r][i];
+          if (t == i) blk[L::kKParams + row * L::kGroups + i] = par[r][i];
+        }
       }
     }
   } else {
@@ -148,40 +132,40 @@ __global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_append_kernel(const Kv
                                    : __ldcs(reinterpret_cast<const uint4*>(src + row * D +
                                                                            64 * h2 + 8 * g));
     }
-    uint32_t word[4][D / 64];
+    uint32_t word[4][D / 64], par[4][D / 64];
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
       for (int h2 = 0; h2 < D / 64; ++h2) {
-        float f[8];
-        unpack8(raw[kk][h2], f);
-        float lo = f[0], hi = f[0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) {
-          lo = fminf(lo, f[e]);
-          hi = fmaxf(hi, f[e]);
-        }
-#pragma unroll
-        for (int s = 4; s < 16; s *= 2) {
-          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, s));
-          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, s));
-        }
-        float scale;
-        const uint32_t par = group_params(lo, hi, scale);
-        word[kk][h2] = transpose_nibbles<2>(quant8(f, lo, scale), g);
-        if (slot[kk] >= 0) {
-          uint32_t* blk = block_of(slot[kk]);
-          const int row = slot[kk] % 16;
-          if ((g & 3) == 0) blk[L::kVParams + row * L::kGroups + 2 * h2 + (g >> 2)] = par;
-          if (!whole) blk[L::v_word(row, h2, g)] = word[kk][h2];
-        }
+        float lo, range;
+        group_range<4>(raw[kk][h2], &lo, &range);
+        word[kk][h2] = transpose_nibbles<2>(quant8(raw[kk][h2], lo, range, &par[kk][h2]), g);
       }
+    // parameters: lanes g = 0 and 4 of a group's four
     if (whole) {
       uint32_t* blk = block_of(base);
 #pragma unroll
-      for (int h2 = 0; h2 < D / 64; ++h2)
+      for (int h2 = 0; h2 < D / 64; ++h2) {
         *reinterpret_cast<uint4*>(blk + L::kVCodes + (h2 * 32 + lane) * 4) =
             make_uint4(word[0][h2], word[1][h2], word[2][h2], word[3][h2]);
+        if ((g & 3) == 0)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            blk[L::kVParams + (8 * (kk >> 1) + 2 * t + (kk & 1)) * L::kGroups + 2 * h2 + (g >> 2)] =
+                par[kk][h2];
+      }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (slot[kk] < 0) continue;
+        uint32_t* blk = block_of(slot[kk]);
+        const int row = slot[kk] % 16;
+#pragma unroll
+        for (int h2 = 0; h2 < D / 64; ++h2) {
+          blk[L::v_word(row, h2, g)] = word[kk][h2];
+          if ((g & 3) == 0) blk[L::kVParams + row * L::kGroups + 2 * h2 + (g >> 2)] = par[kk][h2];
+        }
+      }
     }
   }
 }

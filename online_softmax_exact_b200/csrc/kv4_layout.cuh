@@ -24,7 +24,11 @@
 // parameters, into shared memory.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include <cstdint>
+
+#include "serve_ptx.cuh"
 
 namespace osx {
 
@@ -59,35 +63,93 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t w, int e) {
   return w;
 }
 
-// The eight codes of f against (zero, scale) as one word. The quotient is the correctly
-// rounded one: with r = RN(1/s), q = RN(y r) and e = y - q s (exact by fma), RN(q + e r)
-// is RN(y / s) unless the significand of s is all ones (Markstein's theorem on division
-// by multiplication and fma; s has 8 significant bits here), away from under- and
-// overflow; scales outside that range take a plain division. So a tie is a tie of the
-// true quotient and goes to the even code. Adding 1.5 * 2^23 rounds to the integer in
-// the low bits; the sum of the shifted words carries eight copies of the constant's own
-// bits, which are subtracted at the end (modulo 2^32).
-__device__ __forceinline__ uint32_t quant8(const float (&f)[8], float zero, float scale) {
-  if (!(scale > 0.f)) return 0u;
-  uint32_t w = 0;
-  if (scale >= 0x1p-100f && scale <= 0x1p+100f) {
-    const float r = __frcp_rn(scale);
+// Division by multiplication and fma: with r = RN(1/b), q = RN(a r) and e = a - q b (exact
+// by fma), RN(q + e r) is RN(a / b) away from under- and overflow (Markstein's theorem, for
+// b whose significand is not all ones; here 15, and scales of 8 significant bits).
+__device__ __forceinline__ float divide_fma(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+
+// A group's scale and the codes of eight of its values, in plain divisions: for ranges
+// outside 2^-90 .. 2^90, where the products above could leave the normal numbers.
+__device__ __noinline__ uint32_t quant8_wide(uint4 raw, float zero, float range, float* scale_out) {
+  const float scale = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(range, 15.f)));
+  *scale_out = scale;
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t codes = 0;
+  if (!(scale > 0.f)) return codes;
+  for (int i = 0; i < 8; ++i) {
+    const float f = __uint_as_float((i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    const float q = fminf(fmaxf(rintf(__fdiv_rn(f - zero, scale)), 0.f), 15.f);
+    codes |= (uint32_t)q << (4 * i);
+  }
+  return codes;
+}
+
+// The eight codes of a lane's values (bf16, raw) as one word, against the zero point and the
+// range (maximum - minimum) of their group, and the group's parameter word. A quotient is
+// the correctly rounded one, so a tie is a tie of the true quotient and goes to the even
+// code: adding 1.5 * 2^23 rounds it to the integer in the low bits. The sum of the shifted
+// words carries eight copies of that constant's own bits, subtracted at the end (modulo
+// 2^32). The quotient stays below 15.5 (the scale is at most 2^-8 below range / 15).
+__device__ __forceinline__ uint32_t quant8(const uint4& raw, float zero, float range,
+                                           uint32_t* par) {
+  float scale;
+  uint32_t codes;
+  if (range >= 0x1p-90f && range <= 0x1p+90f) {
+    scale = __bfloat162float(__float2bfloat16_rn(divide_fma(range, 15.f, 1.f / 15.f)));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
+    r = fmaf(fmaf(-scale, r, 1.f), r, r);  // one Newton step
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    codes = 0;
+    // as divide_fma, two values at a time in packed fp32
+    const uint64_t Z = f2_pack(zero, zero), R = f2_pack(r, r), NS = f2_pack(-scale, -scale);
+    const uint64_t ROUND = f2_pack(12582912.0f, 12582912.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = f[i] - zero;
-      const float q0 = y * r;
-      const float q = fmaf(fmaf(-q0, scale, y), r, q0);
-      w += __float_as_uint(q + 12582912.0f) << (4 * i);
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t Y =
+          f2_sub(f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), Z);
+      const uint64_t Q = f2_mul(Y, R);
+      float a, b;
+      f2_unpack(f2_add(f2_fma(f2_fma(Q, NS, Y), R, Q), ROUND), a, b);
+      codes += (__float_as_uint(a) << (8 * i)) + (__float_as_uint(b) << (8 * i + 4));
     }
     constexpr uint32_t kBits = 0x4B400000u;
-    return w - (kBits + (kBits << 4) + (kBits << 8));  // higher shifts leave the word
+    codes -= kBits + (kBits << 4) + (kBits << 8);  // higher shifts leave the word
+  } else {
+    codes = quant8_wide(raw, zero, range, &scale);
   }
+  *par = (__float_as_uint(scale) >> 16) | (__float_as_uint(zero) & 0xffff0000u);
+  return codes;
+}
+
+// Minimum and maximum of eight bf16 values (raw) and of the lanes at kStep and 2 kStep from
+// this one: a group of 32.
+template <int kStep>
+__device__ __forceinline__ void group_range(const uint4& raw, float* lo, float* range) {
+  uint32_t mx, mn, a, b;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(raw.x), "r"(raw.y));
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(raw.z), "r"(raw.w));
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(mx) : "r"(a), "r"(b));
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(raw.x), "r"(raw.y));
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(raw.z), "r"(raw.w));
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(mn) : "r"(a), "r"(b));
+  mn ^= 0x80008000u;  // as maxima of the negated values
+  // low halves in one word, high halves in another: their maximum is (maximum, -minimum)
+  a = __byte_perm(mx, mn, 0x5410);
+  b = __byte_perm(mx, mn, 0x7632);
+  asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = fminf(fmaxf(rintf(__fdiv_rn(f[i] - zero, scale)), 0.f), 15.f);
-    w |= (uint32_t)q << (4 * i);
+  for (int s = kStep; s <= 2 * kStep; s *= 2) {
+    b = __shfl_xor_sync(0xffffffffu, a, s);
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
   }
-  return w;
+  const float hi = __uint_as_float(a << 16);
+  // a minimum of -0 counts as +0: which of the two a minimum of both is, is not defined
+  *lo = 0.f - __uint_as_float(a & 0xffff0000u);
+  *range = hi - *lo;
 }
 
 // scale (low half) and zero point (high half) of a parameter word
