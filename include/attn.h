@@ -419,11 +419,20 @@ int64_t attn_kv4_fwd_workspace(int B, int Hq, int Hkv, int Nq, int d);
  *   o        device, dense [B][Hq][Nq][d], fp32 (o_bf16 = 0) or bf16 (o_bf16 = 1)
  *   lse      device, fp32 [B][Hq][Nq]
  *   window >= 1, sinks >= 0; scale finite, > 0; d in {64, 128}
+ *   workspace  device, 16-byte aligned, at least attn_window_fwd_workspace(...) bytes: a
+ *            call of few query rows splits its keys and joins the parts there. May be NULL
+ *            where that is 0. Its contents on entry do not matter, and nothing in it is
+ *            kept; calls whose work may overlap on the GPU need workspaces of their own.
  */
 attn_status_t attn_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
                               int o_bf16, int B, int Hq, int Hkv, int64_t Nq, int64_t Nkv,
                               int64_t q_ld, int64_t kv_ld, int64_t q_off, int64_t kv_off, int d,
-                              int window, int sinks, float scale, void* stream);
+                              int window, int sinks, float scale, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that attn_window_fwd needs for these sizes (0: none, or sizes it would
+ * refuse). */
+int64_t attn_window_fwd_workspace(int B, int Hq, int Hkv, int64_t Nq, int d);
 
 /*
  * attn_device_status - synchronise `stream` and report whether any kernel of this

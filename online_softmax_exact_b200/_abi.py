@@ -71,8 +71,10 @@ SIGNATURES = {
     "attn_kv4_fwd": (_i32, [_c_void_p] * 7 + [_i32] * 9 + [_i64, _i32, _i32, _f32, _c_void_p,
                                                         _i64, _c_void_p]),
     "attn_kv4_fwd_workspace": (_i64, [_i32] * 5),
-    "attn_window_fwd": (_i32, [_c_void_p] * 5 + [_i32] * 4 + [_i64] * 6 + [_i32, _i32, _i32,
-                                                                           _f32, _c_void_p]),
+    "attn_window_fwd": (_i32, [_c_void_p] * 5 + [_i32] * 4 + [_i64] * 6 + [_i32, _i32, _i32, _f32,
+                                                                           _c_void_p, _i64,
+                                                                           _c_void_p]),
+    "attn_window_fwd_workspace": (_i64, [_i32, _i32, _i32, _i64, _i32]),
     "attn_device_status": (_i32, [_c_void_p, _i32]),
     "attn_debug_inject": (_i32, [_i32, _i32]),
     "attn_debug_wait_timeout": (_i32, [_i64, _c_void_p]),

@@ -24,7 +24,7 @@ SOURCES = ["attn_kernels.cu", "attn_api.cpp", "attn_noalloc.cu", "serve_kernels.
 DEPS = ["sm100_ptx.cuh", "tma_host.h", "attn_fwd_kernel.cuh", "attn_merge_kernel.cuh",
         "attn_internal.h", "api_checks.h", "serve_params.h", "serve_ptx.cuh", "kv_plan_kernel.cuh",
         "qk_norm_rope_kernel.cuh", "kv4_layout.cuh", "kv4_copy_kernels.cuh", "kv4_fwd_kernel.cuh",
-        "attn_window_kernel.cuh"]
+        "decode_common.cuh", "attn_window_kernel.cuh", "window_token_kernel.cuh"]
 
 
 def nvcc() -> str:

@@ -51,6 +51,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "decode_common.cuh"
 #include "kv4_layout.cuh"
 #include "serve_params.h"
 #include "serve_ptx.cuh"
@@ -153,18 +154,6 @@ __device__ __forceinline__ long long block_scan(long long x, long long* scan, lo
   return x + before;
 }
 
-// a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division costs about
-// five times as much, and several of them lie in the path of a short call)
-__device__ __forceinline__ long long divide(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
-
-// Runs that `total` stages are cut into on a grid of `warps` warps: none is empty.
-__device__ __forceinline__ long long kv4_runs(long long total, int warps) {
-  return total < warps ? total : warps;
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(Kv4FwdCfg<D, NT>::kWarps * 32, 1)
 kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
@@ -206,7 +195,7 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
         if (p.B <= kThreads) total = sum;
         if (blockIdx.x == 0 && bb < p.B) p.ws_prefix[bb] = incl - n;  // for the join
         if (base == 0) {
-          const long long runs = kv4_runs(total, gridDim.x * C::kWarps);
+          const long long runs = decode_runs(total, gridDim.x * C::kWarps);
           if (wg < runs) {
             t0 = divide(total * wg, runs);
             t1 = divide(total * (wg + 1), runs);
@@ -689,92 +678,6 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
       }
     }
   }
-}
-
-// Joins the partials of one row of one unit, kHalf of its values: kLanes lanes per partial,
-// the partials dealt to the block's groups of lanes, in two steps whose order does not
-// depend on timing. kThreads: 128, or 512 where a unit has many partials.
-template <int D, int kRows, int kThreads>
-__global__ void __launch_bounds__(kThreads) kv4_join_kernel(
-    const __grid_constant__ Kv4FwdParams p, int n_warps) {
-  constexpr int kHalf = 64, kParts = D / kHalf;  // values of a block, blocks of a row
-  constexpr int kLanes = kHalf / 4, kGroups = kThreads / kLanes;
-  __shared__ float4 part[kGroups][kLanes];
-  __shared__ float stat[kGroups], red[kThreads / 32];
-  const int half = blockIdx.x % kParts;
-  const int unit = blockIdx.x / kParts / kRows, r = blockIdx.x / kParts % kRows;
-  const int per_b = p.Hkv * p.row_tiles;
-  const int b = unit / per_b, in_b = unit - b * per_b;
-  const int h = in_b / p.row_tiles, rt = in_b - h * p.row_tiles;
-  if (rt * kRows + r >= p.rows) return;
-  const long long row = ((long long)b * p.Hkv + h) * p.rows + rt * kRows + r;
-  const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  auto store = [&](float4 y) {
-    const long long at = row * (D / 4) + half * kLanes + lane;
-    if (p.o_bf16)
-      reinterpret_cast<uint2*>(p.o)[at] = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-    else
-      reinterpret_cast<float4*>(p.o)[at] = y;
-  };
-  grid_dependency_wait();  // the attention launch's writes are visible from here on
-  const long long pre = p.ws_prefix[b], end = p.ws_prefix[b + 1], total = p.ws_prefix[p.B];
-  const long long n = divide(end - pre, per_b);  // stages of each of b's units
-  if (n == 0) {  // no key is seen
-    if (grp == 0) store(make_float4(0.f, 0.f, 0.f, 0.f));
-    if (half == 0 && threadIdx.x == 0) p.lse[row] = -INFINITY;
-    return;
-  }
-  // runs of the unit's first and last stage: run w has stages [total w / runs, ..)
-  const long long first = pre + in_b * n, last = first + n - 1;
-  const long long runs = kv4_runs(total, n_warps);
-  const int w0 = (int)divide((first + 1) * runs - 1, total);
-  const int w1 = (int)divide((last + 1) * runs - 1, total);
-  if (w0 == w1) return;  // finished by that warp
-  const int parts = w1 - w0 + 1;
-  const float* ml = p.ws_ml + ((long long)w0 + unit) * (kRows * 2) + 2 * r;
-  const float4* po = reinterpret_cast<const float4*>(p.ws_o + ((long long)w0 + unit) * (kRows * D) +
-                                                     r * D + half * kHalf) + lane;
-  float M = -INFINITY;
-  for (int k = threadIdx.x; k < parts; k += kThreads) M = fmaxf(M, ml[k * (kRows * 2)]);
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) M = fmaxf(M, red[w]);
-  const float base = M == -INFINITY ? 0.f : M;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 5
-  for (int k = grp; k < parts; k += kGroups) {
-    const float2 st = *reinterpret_cast<const float2*>(ml + (long long)k * (kRows * 2));
-    const float4 x = po[(long long)k * (kRows * (D / 4))];
-    const float a = ex2_approx(st.x - base);  // 0 for a part without keys
-    l = fmaf(a, st.y, l);
-    acc.x = fmaf(a, x.x, acc.x);
-    acc.y = fmaf(a, x.y, acc.y);
-    acc.z = fmaf(a, x.z, acc.z);
-    acc.w = fmaf(a, x.w, acc.w);
-  }
-  part[grp][lane] = acc;
-  if (lane == 0) stat[grp] = l;
-  __syncthreads();
-  if (grp != 0) return;
-  float sum = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int k = 0; k < kGroups; ++k) {
-    const float4 x = part[k][lane];
-    sum += stat[k];
-    acc.x += x.x;
-    acc.y += x.y;
-    acc.z += x.z;
-    acc.w += x.w;
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  store(make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  if (half == 0 && lane == 0)
-    p.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
 }  // namespace osx

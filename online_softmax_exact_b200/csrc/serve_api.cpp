@@ -251,10 +251,18 @@ attn_status_t attn_kv4_fwd(const void* q, const void* cache, const int32_t* tabl
                           static_cast<cudaStream_t>(stream)));
 }
 
+int64_t attn_window_fwd_workspace(int B, int Hq, int Hkv, int64_t Nq, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Nq < 1 || Nq > kMaxRows ||
+      (d != 64 && d != 128) || too_many(B, Hq, 1 << 30) || !osx::window_is_token(Hq, Hkv, Nq))
+    return 0;
+  return osx::token_workspace(B, Hkv, (int)(Hq / Hkv * Nq), d).bytes;
+}
+
 attn_status_t attn_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
                               int o_bf16, int B, int Hq, int Hkv, int64_t Nq, int64_t Nkv,
                               int64_t q_ld, int64_t kv_ld, int64_t q_off, int64_t kv_off, int d,
-                              int window, int sinks, float scale, void* stream) {
+                              int window, int sinks, float scale, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
   if (!q || !k || !v || !o || !lse) return ATTN_ERR_INVALID_ARG;
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
   if (Nq < 1 || Nkv < 1 || q_ld < Nq || kv_ld < Nkv || q_off < 0 || kv_off < 0)
@@ -271,12 +279,17 @@ attn_status_t attn_window_fwd(const void* q, const void* k, const void* v, void*
   const Span in[3] = {span(q, ((bh - 1) * q_ld + Nq) * d * 2),
                       span(k, ((bhkv - 1) * kv_ld + Nkv) * d * 2),
                       span(v, ((bhkv - 1) * kv_ld + Nkv) * d * 2)};
-  const Span out[2] = {span(o, bh * Nq * d * (o_bf16 ? 2 : 4)), span(lse, bh * Nq * 4)};
-  if (!apart(out, 2, in, 3)) return ATTN_ERR_INVALID_ARG;
+  const int64_t ws = attn_window_fwd_workspace(B, Hq, Hkv, Nq, d);
+  if (workspace_bytes < ws || (ws > 0 && (!workspace || !aligned(workspace, 16))))
+    return ATTN_ERR_INVALID_ARG;
+  const Span out[3] = {span(o, bh * Nq * d * (o_bf16 ? 2 : 4)), span(lse, bh * Nq * 4),
+                       span(workspace, (uint64_t)ws)};
+  if (!apart(out, ws > 0 ? 3 : 2, in, 3)) return ATTN_ERR_INVALID_ARG;
   const int inj = osx::take_injected();
   if (inj != ATTN_OK) return static_cast<attn_status_t>(inj);
-  const osx::WindowLaunch a{q,  k,    v,     o,     lse,   o_bf16, B, Hq,     Hkv,  Nq,
-                            Nkv, q_ld, kv_ld, q_off, kv_off, d,     window, sinks, scale};
+  const osx::WindowLaunch a{q,    k,     v,     o,      lse, o_bf16, B,     Hq,    Hkv, Nq, Nkv,
+                            q_ld, kv_ld, q_off, kv_off, d,   window, sinks, scale,
+                            static_cast<float*>(workspace)};
   return static_cast<attn_status_t>(osx::launch_window(a, static_cast<cudaStream_t>(stream)));
 }
 

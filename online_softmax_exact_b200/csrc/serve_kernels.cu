@@ -5,11 +5,13 @@
 #include "../../include/attn.h"
 #include "attn_internal.h"
 #include "attn_window_kernel.cuh"
+#include "decode_common.cuh"
 #include "kv4_copy_kernels.cuh"
 #include "kv4_fwd_kernel.cuh"
 #include "kv_plan_kernel.cuh"
 #include "qk_norm_rope_kernel.cuh"
 #include "tma_host.h"
+#include "window_token_kernel.cuh"
 
 namespace osx {
 
@@ -67,13 +69,24 @@ int launch_dependent(void (*kernel)(A...), unsigned grid, unsigned threads, cuda
   return launched();
 }
 
+// The join of a decode launch, 64 values of a row to a block. A unit has about
+// warps / units partials.
+template <int D, int kRows>
+int launch_join(const JoinParams& j, cudaStream_t stream) {
+  const long long units = (long long)j.B * j.Hkv * j.row_tiles;
+  const unsigned grid = grid_1d(units * kRows * (D / 64));
+  if (!grid) return ATTN_ERR_UNSUPPORTED;
+  if (units * 16 >= j.n_warps)
+    return launch_dependent(decode_join_kernel<D, kRows, 128>, grid, 128, stream, j);
+  return launch_dependent(decode_join_kernel<D, kRows, 512>, grid, 512, stream, j);
+}
+
 template <int D, int NT>
 int launch_kv4_fwd_dn(Kv4FwdParams p, long long max_len, int num_sms, cudaStream_t stream) {
   using C = Kv4FwdCfg<D, NT>;
   p.row_tiles = (p.rows + C::kRows - 1) / C::kRows;
   const long long items = (long long)p.B * p.Hkv * p.row_tiles;
-  const unsigned join_grid = grid_1d(items * C::kRows * (D / 64));
-  if (!join_grid) return ATTN_ERR_UNSUPPORTED;
+  if (!grid_1d(items * C::kRows * (D / 64))) return ATTN_ERR_UNSUPPORTED;  // the join's blocks
   // one block per SM, or fewer where there cannot be a stage for each of their warps
   long long keys = max_len;
   if (p.window && (long long)p.window + p.Nq + p.sinks < keys)
@@ -86,12 +99,9 @@ int launch_kv4_fwd_dn(Kv4FwdParams p, long long max_len, int num_sms, cudaStream
   kv4_fwd_kernel<D, NT><<<grid, C::kWarps * 32, C::kSmemBytes, stream>>>(p);
   const int st = launched();
   if (st != ATTN_OK) return st;
-  // a unit has about warps / units partials
-  if (items * 16 >= grid * C::kWarps)
-    return launch_dependent(kv4_join_kernel<D, C::kRows, 128>, join_grid, 128, stream, p,
-                            grid * C::kWarps);
-  return launch_dependent(kv4_join_kernel<D, C::kRows, 512>, join_grid, 512, stream, p,
-                          grid * C::kWarps);
+  const JoinParams j{p.ws_o, p.ws_ml, p.ws_prefix, 0, p.o, p.lse, p.o_bf16, p.B, p.Hkv, p.rows,
+                     p.row_tiles, grid * C::kWarps};
+  return launch_join<D, C::kRows>(j, stream);
 }
 
 template <int D, int NT>
@@ -104,6 +114,64 @@ Kv4Workspace kv4_workspace_dn(int B, int Hkv, int rows) {
   w.o = w.ml + (slots * C::kRows * 2 * 4 + 255) / 256 * 256;
   w.bytes = w.o + slots * C::kRows * D * 4;
   return w;
+}
+
+// Blocks of 16 keys that the rows at positions rel .. rel + Nq - 1 (in key rows) see: those
+// of the sinks, then n_blocks - n_sink_blocks from w0 on.
+void window_blocks(const WindowLaunch& a, TokenParams* p) {
+  const long long rel = a.q_off - a.kv_off;
+  const long long hi = rel + a.Nq < a.Nkv ? rel + a.Nq : a.Nkv;  // keys below may be seen
+  long long lo = rel - a.window + 1;
+  if (lo < 0) lo = 0;
+  long long s = a.sinks - a.kv_off;
+  s = s < 0 ? 0 : (s < a.Nkv ? s : a.Nkv);
+  p->sinks = (int)s;
+  if (s > hi) s = hi;
+  const long long w0 = lo / 16, n_w = hi > lo ? (hi - 1) / 16 - w0 + 1 : 0;
+  long long n_s = s > 0 ? (s + 15) / 16 : 0;
+  if (n_w > 0 && n_s > w0) n_s = w0;
+  p->n_sink_blocks = (int)n_s;
+  p->w0 = (int)(n_w > 0 ? w0 : 0);
+  p->n_blocks = (int)(n_s + n_w);
+}
+
+template <int D, int NT>
+int launch_token_dn(const WindowLaunch& a, const DeviceProps& dp, cudaStream_t stream) {
+  using C = TokenCfg<NT>;
+  TokenParams p;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k = static_cast<const __nv_bfloat16*>(a.k);
+  p.v = static_cast<const __nv_bfloat16*>(a.v);
+  p.o = a.o;
+  p.lse = a.lse;
+  p.o_bf16 = a.o_bf16;
+  p.B = a.B;
+  p.Hkv = a.Hkv;
+  p.Nq = (int)a.Nq;
+  p.rows = (int)(a.Hq / a.Hkv * a.Nq);
+  p.row_tiles = (p.rows + C::kRows - 1) / C::kRows;
+  p.Nkv = (int)a.Nkv;
+  p.q_ld = a.q_ld;
+  p.kv_ld = a.kv_ld;
+  p.rel = a.q_off - a.kv_off;
+  p.window = a.window;
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  window_blocks(a, &p);
+  const long long units = (long long)a.B * a.Hkv * p.row_tiles;
+  if (units > 0x7fffffffLL / C::kRows) return ATTN_ERR_UNSUPPORTED;
+  const TokenWorkspace ws = token_workspace(a.B, a.Hkv, p.rows, D);
+  p.ws_ml = a.workspace;
+  p.ws_o = a.workspace + ws.o / 4;
+  int grid = dp.num_sms < kTokenMaxBlocks ? dp.num_sms : kTokenMaxBlocks;
+  if (units * p.n_blocks < grid) grid = (int)(units * p.n_blocks);
+  if (p.n_blocks > 0) {
+    window_token_kernel<D, NT><<<grid, C::kWarps * 32, 0, stream>>>(p);
+    const int st = launched();
+    if (st != ATTN_OK) return st;
+  }
+  const JoinParams j{p.ws_o,   p.ws_ml, nullptr, p.n_blocks, p.o,         p.lse,
+                     p.o_bf16, p.B,     p.Hkv,   p.rows,     p.row_tiles, grid * C::kWarps};
+  return launch_join<D, C::kRows>(j, stream);
 }
 
 template <int D>
@@ -146,7 +214,26 @@ int launch_window(const WindowLaunch& a, cudaStream_t stream) {
   DeviceProps dp;
   int rc = device_props(&dp);
   if (rc != ATTN_OK) return rc;
+  if (window_is_token(a.Hq, a.Hkv, a.Nq)) {
+    const bool few = a.Hq / a.Hkv * a.Nq <= 4;
+    if (a.d == 128)
+      return few ? launch_token_dn<128, 1>(a, dp, stream) : launch_token_dn<128, 2>(a, dp, stream);
+    return few ? launch_token_dn<64, 1>(a, dp, stream) : launch_token_dn<64, 2>(a, dp, stream);
+  }
   return a.d == 128 ? launch_window_d<128>(a, dp, stream) : launch_window_d<64>(a, dp, stream);
+}
+
+bool window_is_token(int Hq, int Hkv, long long Nq) { return Hq / Hkv * Nq <= kTokenMaxRows; }
+
+TokenWorkspace token_workspace(int B, int Hkv, int rows, int d) {
+  const int tile = rows <= 4 ? TokenCfg<1>::kRows : TokenCfg<2>::kRows;
+  const int warps = rows <= 4 ? TokenCfg<1>::kWarps : TokenCfg<2>::kWarps;
+  const long long units = (long long)B * Hkv * ((rows + tile - 1) / tile);
+  const long long slots = (long long)kTokenMaxBlocks * warps + units;
+  TokenWorkspace w;
+  w.o = (slots * tile * 2 * 4 + 255) / 256 * 256;
+  w.bytes = w.o + slots * tile * d * 4;
+  return w;
 }
 
 int launch_kv_plan(const PlanParams& p, cudaStream_t stream) {

@@ -70,6 +70,33 @@ struct Kv4FwdParams {
   float scale_log2;
 };
 
+// The join of a decode launch's partials (see decode_common.cuh).
+struct JoinParams {
+  const float* parts;       // [slot][kRows][D]
+  const float* ml;          // [slot][kRows][2]
+  const long long* prefix;  // [B + 1] stages before each request's units, or null:
+  long long n_stages;       // every unit has this many
+  void* o;                  // rows of unit (b, h, tile): ((b Hkv + h) rows + tile kRows ..)
+  float* lse;
+  int o_bf16, B, Hkv, rows, row_tiles, n_warps;
+};
+
+// A few query rows over bf16 keys with a window (the token form of attn_window_fwd).
+struct TokenParams {
+  const __nv_bfloat16* q;   // [B][Hq][q_ld][D]
+  const __nv_bfloat16* k;   // [B][Hkv][kv_ld][D]
+  const __nv_bfloat16* v;
+  void* o;
+  float* lse;
+  float* ws_o;
+  float* ws_ml;
+  int o_bf16, B, Hkv, Nq, rows, row_tiles;  // rows = group * Nq
+  int Nkv;
+  long long q_ld, kv_ld, rel;
+  int window, sinks, n_sink_blocks, w0, n_blocks;  // blocks of 16 keys: sinks', then from w0
+  float scale_log2;
+};
+
 struct WindowLaunch {
   const void* q;  // bf16 [B][Hq][q_ld][d], rows [0, Nq)
   const void* k;  // bf16 [B][Hkv][kv_ld][d], rows [0, Nkv)
@@ -81,6 +108,7 @@ struct WindowLaunch {
   int d, window;
   long long sinks;
   float scale;
+  float* workspace;  // of the token form (null where it is not used)
 };
 
 struct WindowParams {

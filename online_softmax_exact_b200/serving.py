@@ -282,9 +282,11 @@ def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, window
     bf16 = _o_type(o_dtype if o is None else o.dtype)
     o = _out(o, (B, Hq, Nq, d), _BF16 if bf16 else _F32, dev, "o")
     lse = _out(lse, (B, Hq, Nq), _F32, dev, "lse")
-    _launch("attn_window_fwd", dev, stream, (q, k, v, o, lse),
+    n_ws = lib().attn_window_fwd_workspace(B, Hq, Hkv, Nq, d)
+    ws = torch.empty(n_ws, dtype=_U8, device=dev) if n_ws else None
+    _launch("attn_window_fwd", dev, stream, (q, k, v, o, lse, ws),
             _arg(q, _BF16, q.shape, "q", dev), _arg(k, _BF16, k.shape, "k", dev),
             _arg(v, _BF16, k.shape, "v", dev), o.data_ptr(), lse.data_ptr(), bf16, B, Hq, Hkv,
             Nq, n, Nq, L, int(q_off), int(kv_off), d, int(window), int(sinks),
-            float(d ** -0.5 if scale is None else scale))
+            float(d ** -0.5 if scale is None else scale), ws.data_ptr() if n_ws else None, n_ws)
     return o, lse

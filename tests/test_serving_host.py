@@ -50,7 +50,8 @@ KV4 = dict(q=G, cache=2 * G, table=3 * G, lens=4 * G, q_pos=None, o=5 * G, lse=6
            Hq=4, Hkv=2, Nq=1, d=64, page=16, n_pages=9, width=4, max_len=0, window=0, sinks=0,
            scale=0.125, ws=8 * G, ws_bytes=1 << 24, stream=None)
 WIN = dict(q=G, k=2 * G, v=3 * G, o=4 * G, lse=5 * G, o_bf16=0, B=2, Hq=4, Hkv=2, Nq=8, Nkv=16,
-           q_ld=8, kv_ld=16, q_off=8, kv_off=0, d=64, window=4, sinks=1, scale=0.125, stream=None)
+           q_ld=8, kv_ld=16, q_off=8, kv_off=0, d=64, window=4, sinks=1, scale=0.125,
+           ws=6 * G, ws_bytes=1 << 24, stream=None)
 
 INVALID = {
     "attn_kv_plan": (PLAN, [
@@ -86,7 +87,8 @@ INVALID = {
         dict(lse=5 * G + 2), dict(B=0), dict(Hq=3), dict(Hkv=0), dict(Nq=0), dict(Nkv=0),
         dict(q_ld=7), dict(kv_ld=15), dict(q_off=-1), dict(kv_off=-1), dict(o_bf16=3),
         dict(window=0), dict(window=-4), dict(sinks=-1), dict(scale=0.0), dict(scale=-0.5),
-        dict(scale=float("nan")), dict(o=G), dict(lse=4 * G), dict(o=3 * G - 4096)]),
+        dict(scale=float("nan")), dict(o=G), dict(lse=4 * G), dict(o=3 * G - 4096), dict(ws=None),
+        dict(ws=6 * G + 4), dict(ws_bytes=1 << 16), dict(ws=G), dict(ws=5 * G - 64)]),
 }
 UNSUPPORTED = {
     "attn_kv_plan": (PLAN, [dict(B=1 << 20, n_new=1 << 12), dict(width=1 << 20, page=1 << 12)]),
@@ -130,6 +132,19 @@ def test_kv4_workspace(lib):
     invalid, _ = statuses()
     assert call(lib.attn_kv4_fwd, KV4, ws_bytes=need - 1) == invalid
     assert 0 < need < size(2, 4, 2, 1, 128) < size(200, 32, 8, 1, 128) < 1 << 25
+
+
+def test_window_workspace(lib):
+    """Needed for few query rows only; a call without that need takes a null one."""
+    size = lib.attn_window_fwd_workspace
+    for bad in ((0, 4, 2, 1, 64), (1, 3, 2, 1, 64), (1, 4, 2, 0, 64), (1, 4, 2, 1, 96)):
+        assert size(*bad) == 0
+    assert 0 < size(1, 4, 2, 1, 64) < size(1, 4, 2, 1, 128) < 1 << 24
+    assert size(1, 4, 2, 4096, 128) == 0
+    invalid, _ = statuses()
+    need = size(2, 4, 2, 8, 64)
+    assert call(lib.attn_window_fwd, WIN, ws_bytes=need - 1) == invalid
+    assert call(lib.attn_window_fwd, WIN, Nq=300, q_ld=300, ws=None, ws_bytes=0) not in statuses()
 
 
 @pytest.mark.parametrize("entry", sorted(DEFAULTS))
