@@ -9,6 +9,7 @@ import ctypes
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().parent / "libattn.so"
+BINDING_PATH = Path(__file__).resolve().parent / "_serving.so"
 
 ATTN_OK = 0
 ATTN_ERR_INVALID_ARG = 1
@@ -107,3 +108,29 @@ def load() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = lib
     return _lib
+
+
+_serving = None
+
+
+def load_serving():
+    """The native binding of the serving operators (built by ``build.py``)."""
+    global _serving
+    if _serving is None:
+        import importlib.machinery
+        import importlib.util
+
+        if not BINDING_PATH.exists():
+            raise ImportError(
+                f"{BINDING_PATH} is missing: build it with `python -m"
+                " online_softmax_exact_b200.build` (there is no fallback implementation)")
+        load()
+        import torch  # noqa: F401  (the binding uses its libraries)
+
+        loader = importlib.machinery.ExtensionFileLoader("_serving", str(BINDING_PATH))
+        spec = importlib.util.spec_from_file_location("_serving", BINDING_PATH, loader=loader)
+        mod = importlib.util.module_from_spec(spec)
+        loader.exec_module(mod)
+        mod.set_error(AttnError)
+        _serving = mod
+    return _serving

@@ -16,6 +16,8 @@ CSRC = PKG / "csrc"
 ROOT = PKG.parent
 BUILD = ROOT / "_build"
 LIB = PKG / "libattn.so"
+BINDING = PKG / "_serving.so"  # the serving operators' torch binding, linked to libattn.so
+BINDING_SOURCE = "serving_binding.cpp"
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -32,18 +34,46 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _stale() -> bool:
-    if not LIB.exists():
+def _stale(out: Path, sources) -> bool:
+    if not out.exists():
         return True
-    t = LIB.stat().st_mtime
-    files = [CSRC / s for s in SOURCES + DEPS] + [ROOT / "include" / "attn.h"]
+    t = out.stat().st_mtime
+    files = [CSRC / s for s in sources] + [ROOT / "include" / "attn.h"]
     return any(f.stat().st_mtime > t for f in files)
 
 
 def build(force: bool = False, verbose: bool = False) -> Path:
-    """Compile every CUDA source for sm_100a and link libattn.so next to this file."""
-    if not force and not _stale():
-        return LIB
+    """Compile every CUDA source for sm_100a, link libattn.so next to this file, and the
+    serving operators' torch binding beside it."""
+    if force or _stale(LIB, SOURCES + DEPS):
+        _build_lib(verbose)
+    if force or _stale(BINDING, [BINDING_SOURCE]):
+        _build_binding()
+    return LIB
+
+
+def _build_binding() -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    cxx = os.environ.get("CXX") or "g++"
+    libs = library_paths(device_type="cuda")
+    tmp = BINDING.with_suffix(f".{os.getpid()}.tmp.so")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unknown-pragmas",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-isystem{p}" for p in include_paths(device_type="cuda")],
+           f"-isystem{sysconfig.get_paths()['include']}", str(CSRC / BINDING_SOURCE), "-o", str(tmp),
+           *[f"-L{p}" for p in libs], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch",
+           "-ltorch_python", f"-L{PKG}", "-l:libattn.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
+def _build_lib(verbose: bool) -> None:
     BUILD.mkdir(exist_ok=True)
     objs = []
     for src in SOURCES:
@@ -63,7 +93,6 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
