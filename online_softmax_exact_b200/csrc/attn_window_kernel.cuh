@@ -71,10 +71,27 @@ __device__ __forceinline__ WindowTile window_tile(const WindowParams& p, int row
   return w;
 }
 
+// Unit u's head and row block. First the row blocks whose windows lie whole inside the
+// sequence (all of one cost), head by head, so that the CTAs running at one time share a
+// few heads' keys in L2; then those that the sequence's start cuts, longest first, so that
+// the grid's last units are its shortest. (Measured: 2 x 16 heads of 4001 rows, window
+// 1024, 103 us with row blocks in order, 93 us like this.)
+__device__ __forceinline__ void window_place(const WindowParams& p, int u, int* bh, int* qp) {
+  const int n_full = p.row_blocks - p.cut_blocks;
+  const int full = p.heads * n_full;
+  if (u < full) {
+    *bh = u / n_full;
+    *qp = p.row_blocks - 1 - (u - *bh * n_full);
+  } else {
+    const int r = (u - full) / p.heads;
+    *qp = p.cut_blocks - 1 - r;
+    *bh = u - full - r * p.heads;
+  }
+}
+
 __device__ __forceinline__ WindowUnit window_unit(const WindowParams& p, int u) {
   WindowUnit un;
-  un.bh = u / p.row_blocks;
-  un.qp = u - un.bh * p.row_blocks;
+  window_place(p, u, &un.bh, &un.qp);
   un.t[0] = window_tile(p, un.qp * 256);
   un.t[1] = window_tile(p, un.qp * 256 + 128);
   const WindowTile &a = un.t[0], &b = un.t[1];
@@ -158,7 +175,8 @@ attn_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             // Q.K^T)
             const int u2 = unit_for_round(r + 1, blockIdx.x, G);
             if (u2 < p.units) {
-              const int bh2 = u2 / p.row_blocks, qp2 = u2 - bh2 * p.row_blocks;
+              int bh2, qp2;
+              window_place(p, u2, &bh2, &qp2);
               for (int t = 0; t < 2; ++t)
                 for (int h = 0; h < D / 64; ++h)
                   tma_prefetch_l2_3d(&tmQ, h * 64, qp2 * 256 + t * 128, bh2);

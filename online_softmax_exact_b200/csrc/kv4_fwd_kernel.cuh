@@ -168,6 +168,7 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
   const uint32_t bar0 = smem_u32(smem + C::kBarOff) + warp * C::kStages * 8;
   long long* scan = reinterpret_cast<long long*>(smem + C::kScanOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
+  grid_dependents_launch();
   if (lane == 0) {
     for (int s = 0; s < C::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
     fence_mbar_init();

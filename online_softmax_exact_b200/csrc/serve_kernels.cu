@@ -201,6 +201,10 @@ int launch_window_d(const WindowLaunch& a, const DeviceProps& dp, cudaStream_t s
   const long long units = (long long)a.B * a.Hq * p.row_blocks;
   if (units > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   p.units = (int)units;
+  p.heads = a.B * a.Hq;
+  long long cut = (a.window - 1 - p.rel + 255) / 256;  // 256 qp < window - 1 - rel
+  if (a.window - 1 - p.rel <= 0) cut = 0;
+  p.cut_blocks = (int)(cut < p.row_blocks ? cut : p.row_blocks);
   const int rc = prepare_kernel<attn_window_kernel<D>>(C::kSmemBytes, false);
   if (rc != ATTN_OK) return rc;
   const int grid = units < dp.num_sms ? (int)units : dp.num_sms;

@@ -119,7 +119,8 @@ struct WindowParams {
   int Nq, Nkv;
   long long rel;     // position of query row 0 less that of key row 0
   int window, sinks; // sinks: key rows [0, sinks) of this chunk stay visible
-  int row_blocks, units;
+  int heads, row_blocks, units;  // heads: B Hq
+  int cut_blocks;  // row blocks whose windows the sequence's start cuts
   float scale_log2;
 };
 
