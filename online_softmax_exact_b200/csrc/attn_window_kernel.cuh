@@ -153,6 +153,8 @@ attn_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dependents_launch();
+  grid_dependency_wait();
   const uint32_t tmem = *tmem_slot;
   const int G = gridDim.x;
 

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(
   constexpr int kHalf = 64, kParts = D / kHalf;  // values of a block, blocks of a row
   constexpr int kLanes = kHalf / 4, kGroups = kThreads / kLanes;
   __shared__ float4 part[kGroups][kLanes];
-  __shared__ float stat[kGroups], red[kThreads / 32];
+  __shared__ float2 stat[kGroups];
   const int half = blockIdx.x % kParts;
   const int unit = blockIdx.x / kParts / kRows, r = blockIdx.x / kParts % kRows;
   const int per_b = p.Hkv * p.row_tiles;
@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(
   const int h = in_b / p.row_tiles, rt = in_b - h * p.row_tiles;
   if (rt * kRows + r >= p.rows) return;
   const long long row = ((long long)b * p.Hkv + h) * p.rows + rt * kRows + r;
+  grid_dependents_launch();
   const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   auto store = [&](float4 y) {
     const long long at = row * (D / 4) + half * kLanes + lane;
@@ -83,42 +84,59 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(
   const float* ml = p.ml + ((long long)w0 + unit) * (kRows * 2) + 2 * r;
   const float4* po = reinterpret_cast<const float4*>(p.parts + ((long long)w0 + unit) * (kRows * D) +
                                                      r * D + half * kHalf) + lane;
-  float M = -INFINITY;
-  for (int k = threadIdx.x; k < parts; k += kThreads) M = fmaxf(M, ml[k * (kRows * 2)]);
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) M = fmaxf(M, red[w]);
-  const float base = M == -INFINITY ? 0.f : M;
+  // this group's partials against their own running maximum
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 5
-  for (int k = grp; k < parts; k += kGroups) {
-    const float2 st = *reinterpret_cast<const float2*>(ml + (long long)k * (kRows * 2));
-    const float4 x = po[(long long)k * (kRows * (D / 4))];
-    const float a = ex2_approx(st.x - base);  // 0 for a part without keys
-    l = fmaf(a, st.y, l);
-    acc.x = fmaf(a, x.x, acc.x);
-    acc.y = fmaf(a, x.y, acc.y);
-    acc.z = fmaf(a, x.z, acc.z);
-    acc.w = fmaf(a, x.w, acc.w);
+  float M = -INFINITY, l = 0.f;
+  for (int k0 = grp; k0 < parts; k0 += 5 * kGroups) {
+    float2 st[5];
+    float4 x[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+      const long long k = k0 + j * kGroups;
+      st[j] = make_float2(-INFINITY, 0.f);
+      x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < parts) {
+        st[j] = *reinterpret_cast<const float2*>(ml + k * (kRows * 2));
+        x[j] = po[k * (kRows * (D / 4))];
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int j = 0; j < 5; ++j) top = fmaxf(top, st[j].x);
+    if (top == -INFINITY) continue;  // no keys so far
+    const float keep = ex2_approx(M - top);
+    M = top;
+    l *= keep;
+    acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+      const float a = ex2_approx(st[j].x - top);  // 0 for a part without keys
+      l = fmaf(a, st[j].y, l);
+      acc.x = fmaf(a, x[j].x, acc.x);
+      acc.y = fmaf(a, x[j].y, acc.y);
+      acc.z = fmaf(a, x[j].z, acc.z);
+      acc.w = fmaf(a, x[j].w, acc.w);
+    }
   }
   part[grp][lane] = acc;
-  if (lane == 0) stat[grp] = l;
+  if (lane == 0) stat[grp] = make_float2(M, l);
   __syncthreads();
   if (grp != 0) return;
+  M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) M = fmaxf(M, stat[k].x);
+  const float base = M == -INFINITY ? 0.f : M;
   float sum = 0.f;
   acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < kGroups; ++k) {
+    const float a = ex2_approx(stat[k].x - base);
     const float4 x = part[k][lane];
-    sum += stat[k];
-    acc.x += x.x;
-    acc.y += x.y;
-    acc.z += x.z;
-    acc.w += x.w;
+    sum = fmaf(a, stat[k].y, sum);
+    acc.x = fmaf(a, x.x, acc.x);
+    acc.y = fmaf(a, x.y, acc.y);
+    acc.z = fmaf(a, x.z, acc.z);
+    acc.w = fmaf(a, x.w, acc.w);
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   store(make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));

@@ -43,6 +43,8 @@ __global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_append_kernel(const Kv
   int b, c, h, which;
   if (!kv4_copy_item(p, b, c, h, which)) return;
   const int lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
+  grid_dependents_launch();
+  grid_dependency_wait();
   const int* slots = p.slots + (long long)b * p.N;
   const long long limit = (long long)p.n_pages * p.page_size;
   // the window's first token: aligned with the cache's blocks if slots run on from the first
@@ -188,6 +190,8 @@ __global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_read_kernel(const Kv4C
   int b, c, h, which;
   if (!kv4_copy_item(p, b, c, h, which)) return;
   const int lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
+  grid_dependents_launch();
+  grid_dependency_wait();
   const int start = p.start[b], len = p.lens[b];
   const int blocks = p.page_size / 16;
   const long long pb = (long long)(start > 0 ? start : 0) / 16 + c;  // block of the request

@@ -74,7 +74,7 @@ struct Kv4FwdCfg {
   static constexpr uint32_t kCursorOff = kScanOff;  // [2 warps], after the scan
   static constexpr uint32_t kMiscOff = kScanOff + (kWarps * 32 + kWarps) * 8;
   static_assert(kWarps * 2 * 64 <= kWarps * 32 * 8, "cursors fit the scan's place");
-  static constexpr uint32_t kSmemBytes = kMiscOff + 16;
+  static constexpr uint32_t kSmemBytes = kMiscOff + kWarps * 4;
   static_assert(kStages * kSB <= 31, "block masks");
   static_assert(kSmemBytes <= 232448, "shared memory per block");
 };
@@ -167,61 +167,89 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
   const uint32_t ring_u = smem_u32(ring);
   const uint32_t bar0 = smem_u32(smem + C::kBarOff) + warp * C::kStages * 8;
   long long* scan = reinterpret_cast<long long*>(smem + C::kScanOff);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
-  grid_dependents_launch();
+  // (each warp has a flag of its own: no warp waits for another)
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff) + warp;
   if (lane == 0) {
+    *abort_flag = 0;
     for (int s = 0; s < C::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) *abort_flag = 0;
+  __syncwarp();
+  grid_dependents_launch();
+  grid_dependency_wait();
 
   // ---- this warp's run of stages: [t0, t1) of the units' stages, one unit after another
   // (no more runs than stages; neighbouring runs lie on different SMs, so that few of them
   // spread over the card)
   const long long wg = (long long)warp * gridDim.x + blockIdx.x;
   const int per_b = p.Hkv * p.row_tiles;  // units of a request
+  const int warps = gridDim.x * C::kWarps;
+  auto stages_of = [&](int bb) {  // of all of request bb's units
+    return bb < p.B ? (long long)((kv4_span(p, bb).n_blocks + C::kSB - 1) / C::kSB) * per_b : 0ll;
+  };
   long long total = 0, t0 = 0, t1 = 0, pre = 0;
   int b = 0;
-  for (int pass = p.B > kThreads ? 0 : 1; pass < 2; ++pass) {
-    // (more requests than threads: a first pass for the total)
-    long long carry = 0;
-    bool found = false;
-    for (int base = 0; base < p.B; base += kThreads) {
-      const int bb = base + threadIdx.x;
-      const long long n =
-          bb < p.B ? (long long)((kv4_span(p, bb).n_blocks + C::kSB - 1) / C::kSB) * per_b : 0;
-      long long sum;
-      const long long incl = carry + block_scan<C::kWarps>(n, scan + kThreads, &sum);
-      if (pass == 1) {
-        if (p.B <= kThreads) total = sum;
-        if (blockIdx.x == 0 && bb < p.B) p.ws_prefix[bb] = incl - n;  // for the join
-        if (base == 0) {
-          const long long runs = decode_runs(total, gridDim.x * C::kWarps);
-          if (wg < runs) {
-            t0 = divide(total * wg, runs);
-            t1 = divide(total * (wg + 1), runs);
-          }
-        }
-        scan[threadIdx.x] = incl;
-        __syncthreads();
-        if (!found && t0 < t1 && t0 < carry + sum) {
-          // the first request whose stages end behind t0
-          int lo = 0, hi = kThreads - 1;
-          while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (scan[mid] > t0) hi = mid; else lo = mid + 1;
-          }
-          b = base + lo;
-          pre = lo > 0 ? scan[lo - 1] : carry;
-          found = true;
-        }
-      }
-      carry += sum;
+  auto cut = [&]() {
+    const long long runs = decode_runs(total, warps);
+    if (wg < runs) {
+      t0 = divide(total * wg, runs);
+      t1 = divide(total * (wg + 1), runs);
     }
-    if (pass == 0) total = carry;
-    if (pass == 1 && blockIdx.x == 0 && threadIdx.x == 0) p.ws_prefix[p.B] = total;
+  };
+  if (p.B <= 32) {  // within the warp
+    const long long n = stages_of(lane);
+    long long incl = n;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += y;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    if (blockIdx.x == 0 && warp == 0) {  // for the join
+      if (lane < p.B) p.ws_prefix[lane] = incl - n;
+      if (lane == 0) p.ws_prefix[p.B] = total;
+    }
+    cut();
+    // the first request whose stages end behind t0
+    const uint32_t behind = __ballot_sync(0xffffffffu, incl > t0);
+    if (t0 < t1) {
+      b = __ffs(behind) - 1;
+      pre = __shfl_sync(0xffffffffu, incl - n, b);
+    }
+  } else {
+    for (int pass = p.B > kThreads ? 0 : 1; pass < 2; ++pass) {
+      // (more requests than threads: a first pass for the total)
+      long long carry = 0;
+      bool found = false;
+      for (int base = 0; base < p.B; base += kThreads) {
+        const int bb = base + threadIdx.x;
+        const long long n = stages_of(bb);
+        long long sum;
+        const long long incl = carry + block_scan<C::kWarps>(n, scan + kThreads, &sum);
+        if (pass == 1) {
+          if (p.B <= kThreads) total = sum;
+          if (blockIdx.x == 0 && bb < p.B) p.ws_prefix[bb] = incl - n;
+          if (base == 0) cut();
+          scan[threadIdx.x] = incl;
+          __syncthreads();
+          if (!found && t0 < t1 && t0 < carry + sum) {
+            int lo = 0, hi = kThreads - 1;
+            while (lo < hi) {
+              const int mid = (lo + hi) / 2;
+              if (scan[mid] > t0) hi = mid; else lo = mid + 1;
+            }
+            b = base + lo;
+            pre = lo > 0 ? scan[lo - 1] : carry;
+            found = true;
+          }
+        }
+        carry += sum;
+      }
+      if (pass == 0) total = carry;
+      if (pass == 1 && blockIdx.x == 0 && threadIdx.x == 0) p.ws_prefix[p.B] = total;
+    }
+    __syncthreads();  // the cursors take the scan's place
   }
-  __syncthreads();  // barriers and abort flag are initialised
   if (t0 >= t1) return;
 
   // ---- two cursors over the run: where to compute, and where to fetch. They live in shared

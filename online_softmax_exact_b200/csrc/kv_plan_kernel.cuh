@@ -19,6 +19,7 @@
 #include <cstdint>
 
 #include "serve_params.h"
+#include "serve_ptx.cuh"
 
 namespace osx {
 
@@ -55,6 +56,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
   const long long t0 = (long long)blockIdx.x * kPlanChunk;
   const long long t1 = t0 + kPlanChunk < total ? t0 + kPlanChunk : total;
   const int b0 = (int)(t0 / p.n_new), b1 = (int)((t1 - 1) / p.n_new);  // requests of the chunk
+  grid_dependents_launch();
+  grid_dependency_wait();
   const int head = *p.free_head;
 
   long long carry = 0;  // needs of the requests before the current batch of 512

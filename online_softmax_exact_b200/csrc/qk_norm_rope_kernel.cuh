@@ -103,6 +103,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(
   int pos = 0;
 #pragma unroll
   for (int a = 0; a < kAhead; ++a) x[a][0] = x[a][1] = make_uint2(0, 0);
+  grid_dependents_launch();
+  grid_dependency_wait();
   if (token < total) {
     src = token_rows(token);
     pos = p.positions[token];

@@ -23,6 +23,29 @@ int launched() {
   return ATTN_OK;
 }
 
+// A launch whose blocks may start before the launch before it in the stream has ended (each
+// waits for that in the kernel before it touches global memory): its launch latency and
+// set-up lie beside that one's end.
+template <class... A>
+int launch_dependent(void (*kernel)(A...), unsigned grid, unsigned threads, uint32_t smem,
+                     cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_ERR_CUDA;
+  }
+  return launched();
+}
+
 // Blocks of a one-dimensional grid, or 0 when there are more than a grid can have.
 unsigned grid_1d(long long blocks) {
   return blocks > 0 && blocks <= 0x7fffffffLL ? static_cast<unsigned>(blocks) : 0u;
@@ -48,27 +71,6 @@ int prepare_kernel(uint32_t smem, bool clusters) {
   return ATTN_OK;
 }
 
-// A launch whose blocks may start before the launch before it in the stream has ended (they
-// wait for it in the kernel): its launch latency and set-up lie beside that one's end.
-template <class... A>
-int launch_dependent(void (*kernel)(A...), unsigned grid, unsigned threads, cudaStream_t stream,
-                     A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
-    cudaGetLastError();
-    return ATTN_ERR_CUDA;
-  }
-  return launched();
-}
-
 // The join of a decode launch, 64 values of a row to a block. A unit has about
 // warps / units partials.
 template <int D, int kRows>
@@ -77,8 +79,8 @@ int launch_join(const JoinParams& j, cudaStream_t stream) {
   const unsigned grid = grid_1d(units * kRows * (D / 64));
   if (!grid) return ATTN_ERR_UNSUPPORTED;
   if (units * 16 >= j.n_warps)
-    return launch_dependent(decode_join_kernel<D, kRows, 128>, grid, 128, stream, j);
-  return launch_dependent(decode_join_kernel<D, kRows, 512>, grid, 512, stream, j);
+    return launch_dependent(decode_join_kernel<D, kRows, 128>, grid, 128, 0, stream, j);
+  return launch_dependent(decode_join_kernel<D, kRows, 512>, grid, 512, 0, stream, j);
 }
 
 template <int D, int NT>
@@ -96,8 +98,8 @@ int launch_kv4_fwd_dn(Kv4FwdParams p, long long max_len, int num_sms, cudaStream
   if (stages < grid) grid = (int)stages;
   const int rc = prepare_kernel<kv4_fwd_kernel<D, NT>>(C::kSmemBytes, false);
   if (rc != ATTN_OK) return rc;
-  kv4_fwd_kernel<D, NT><<<grid, C::kWarps * 32, C::kSmemBytes, stream>>>(p);
-  const int st = launched();
+  const int st =
+      launch_dependent(kv4_fwd_kernel<D, NT>, grid, C::kWarps * 32, C::kSmemBytes, stream, p);
   if (st != ATTN_OK) return st;
   const JoinParams j{p.ws_o, p.ws_ml, p.ws_prefix, 0, p.o, p.lse, p.o_bf16, p.B, p.Hkv, p.rows,
                      p.row_tiles, grid * C::kWarps};
@@ -165,8 +167,7 @@ int launch_token_dn(const WindowLaunch& a, const DeviceProps& dp, cudaStream_t s
   int grid = dp.num_sms < kTokenMaxBlocks ? dp.num_sms : kTokenMaxBlocks;
   if (units * p.n_blocks < grid) grid = (int)(units * p.n_blocks);
   if (p.n_blocks > 0) {
-    window_token_kernel<D, NT><<<grid, C::kWarps * 32, 0, stream>>>(p);
-    const int st = launched();
+    const int st = launch_dependent(window_token_kernel<D, NT>, grid, C::kWarps * 32, 0, stream, p);
     if (st != ATTN_OK) return st;
   }
   const JoinParams j{p.ws_o,   p.ws_ml, nullptr, p.n_blocks, p.o,         p.lse,
@@ -208,8 +209,8 @@ int launch_window_d(const WindowLaunch& a, const DeviceProps& dp, cudaStream_t s
   const int rc = prepare_kernel<attn_window_kernel<D>>(C::kSmemBytes, false);
   if (rc != ATTN_OK) return rc;
   const int grid = units < dp.num_sms ? (int)units : dp.num_sms;
-  attn_window_kernel<D><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
-  return launched();
+  return launch_dependent(attn_window_kernel<D>, grid, C::kThreads, C::kSmemBytes, stream, tq, tk,
+                          tv, p);
 }
 
 }  // namespace
@@ -246,8 +247,7 @@ int launch_kv_plan(const PlanParams& p, cudaStream_t stream) {
   if (rc != ATTN_OK) return rc;
   const unsigned grid = grid_1d(((long long)p.B * p.n_new + kPlanChunk - 1) / kPlanChunk);
   if (!grid) return ATTN_ERR_UNSUPPORTED;
-  kv_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(p);
-  return launched();
+  return launch_dependent(kv_plan_kernel, grid, kPlanThreads, 0, stream, p);
 }
 
 int launch_qk_norm_rope(const RopeParams& p, int d, int interleaved, cudaStream_t stream) {
@@ -263,8 +263,7 @@ int launch_qk_norm_rope(const RopeParams& p, int d, int interleaved, cudaStream_
   const unsigned grid = grid_1d(blocks < most ? blocks : most);
   auto* kernel = d == 128 ? (interleaved ? qk_norm_rope_kernel<128, true> : qk_norm_rope_kernel<128, false>)
                           : (interleaved ? qk_norm_rope_kernel<64, true> : qk_norm_rope_kernel<64, false>);
-  kernel<<<grid, kRopeThreads, 0, stream>>>(p, split);
-  return launched();
+  return launch_dependent(kernel, grid, kRopeThreads, 0, stream, p, split);
 }
 
 int launch_kv4_append(const Kv4CopyParams& p, int d, cudaStream_t stream) {
@@ -274,11 +273,8 @@ int launch_kv4_append(const Kv4CopyParams& p, int d, cudaStream_t stream) {
   const unsigned grid =
       grid_1d(((long long)p.B * p.windows * p.Hkv * 2 + kKv4CopyWarps - 1) / kKv4CopyWarps);
   if (!grid) return ATTN_ERR_UNSUPPORTED;
-  if (d == 128)
-    kv4_append_kernel<128><<<grid, kKv4CopyWarps * 32, 0, stream>>>(p);
-  else
-    kv4_append_kernel<64><<<grid, kKv4CopyWarps * 32, 0, stream>>>(p);
-  return launched();
+  return launch_dependent(d == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>, grid,
+                          kKv4CopyWarps * 32, 0, stream, p);
 }
 
 int launch_kv4_read(const Kv4CopyParams& p, int d, cudaStream_t stream) {
@@ -288,11 +284,8 @@ int launch_kv4_read(const Kv4CopyParams& p, int d, cudaStream_t stream) {
   const unsigned grid =
       grid_1d(((long long)p.B * p.windows * p.Hkv * 2 + kKv4CopyWarps - 1) / kKv4CopyWarps);
   if (!grid) return ATTN_ERR_UNSUPPORTED;
-  if (d == 128)
-    kv4_read_kernel<128><<<grid, kKv4CopyWarps * 32, 0, stream>>>(p);
-  else
-    kv4_read_kernel<64><<<grid, kKv4CopyWarps * 32, 0, stream>>>(p);
-  return launched();
+  return launch_dependent(d == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>, grid,
+                          kKv4CopyWarps * 32, 0, stream, p);
 }
 
 // 4 query rows a unit, or 8 (the unpacked codes then serve twice the rows)

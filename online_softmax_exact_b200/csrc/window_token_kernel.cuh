@@ -84,6 +84,7 @@ window_token_kernel(const __grid_constant__ TokenParams p) {
                         : make_uint4(0, 0, 0, 0);
     }
   };
+  grid_dependency_wait();
   load_k(unit, blk);
   load_v(unit, blk);
 
