@@ -60,10 +60,17 @@ namespace osx {
 
 template <int D, int NT>
 struct Kv4FwdCfg {
-    static constexpr int kWarps = NT == 1 ? 16 : 8;   // 128 or 255 registers a thread
+    // Eight warps of 255 registers, so that a stage's blocks run interleaved. Measured at
+  // NT = 1, d = 128 (128k tokens / ragged batch of 32, us): 8 warps, stages of 4 blocks 40.7
+  // / 56.0; 16 warps, stages of 2 (a block at a time in registers) 42.8 / 57.2; 12 warps,
+  // stages of 3 42.0 / 56.5; the same ring without any compute 33.1 / 45.9.
+  static constexpr int kWarps = 8;
   static constexpr int kRows = 4 * NT;
-  static constexpr int kSB = D == 128 ? 2 : 4;      // blocks of 16 tokens per stage
-  static constexpr int kStages = NT == 1 ? 2 : 4;
+  static constexpr int kSB = D == 128 && NT == 2 ? 2 : 4;  // blocks of 16 tokens per stage
+  static constexpr int kStages = D == 128 && NT == 1 ? 2 : 4;
+  // Two row tiles leave no registers for blocks side by side: a branch per block, taken or
+  // not, keeps the next block's operands out of them.
+  static constexpr bool kBlockBranch = NT == 2;
   static constexpr uint32_t kStageBytes = kSB * Kv4<D>::kBytes;
   static constexpr uint32_t kWarpBytes = kStages * kStageBytes;
   // each warp's queries as B operands, 16 bytes a lane, tile and group
@@ -446,18 +453,17 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
       ++waited;
       const uint8_t* stage = ring + slot * C::kStageBytes;
       const uint32_t present = masks >> (C::kSB * slot);
-      const bool inside = st >= in_lo && st < in_hi;
+      constexpr uint32_t kAll = (1u << C::kSB) - 1u;
+      const bool inside = st >= in_lo && st < in_hi && (present & kAll) == kAll;
       auto compute = [&](auto edge) {
         constexpr bool kEdge = decltype(edge)::value;
         // ---- scores
         float sc[C::kSB][NT][2];  // keys g and g + 8 of a block
 #pragma unroll
         for (int j = 0; j < C::kSB; ++j) {
-          // (a branch per block, taken or not, also keeps the next block's operands out of the
-          // registers)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) sc[j][nt][0] = sc[j][nt][1] = -INFINITY;
-          if (!((present >> j) & 1u)) continue;
+          if ((kEdge || C::kBlockBranch) && !((present >> j) & 1u)) continue;
           const uint32_t* blk = reinterpret_cast<const uint32_t*>(stage + j * L::kBytes);
           uint32_t w[2][kG], par[2][kG];
           if constexpr (D == 128) {
@@ -564,7 +570,7 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
         // ---- P, and O^T += V^T P^T block by block
 #pragma unroll
         for (int j = 0; j < C::kSB; ++j) {
-          if (!((present >> j) & 1u)) continue;
+          if ((kEdge || C::kBlockBranch) && !((present >> j) & 1u)) continue;
           const uint32_t* blk = reinterpret_cast<const uint32_t*>(stage + j * L::kBytes);
           float pr[NT][2];
 #pragma unroll
