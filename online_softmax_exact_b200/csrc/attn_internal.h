@@ -60,12 +60,11 @@ struct WindowLaunch;
 int launch_window(const WindowLaunch& a, cudaStream_t stream);
 // Whether a windowed call runs in its token form, and that form's workspace (statistics at
 // offset 0, rows at o).
-constexpr int kTokenMaxRows = 32;     // query rows of a key/value head at most
 constexpr int kTokenMaxBlocks = 160;  // blocks of the attention launch at most
 struct TokenWorkspace {
   long long o, bytes;
 };
-bool window_is_token(int Hq, int Hkv, long long Nq);
+bool window_is_token(int B, int Hq, int Hkv, long long Nq);
 TokenWorkspace token_workspace(int B, int Hkv, int rows, int d);
 int launch_kv_plan(const PlanParams& p, cudaStream_t stream);
 int launch_qk_norm_rope(const RopeParams& p, int d, int interleaved, cudaStream_t stream);

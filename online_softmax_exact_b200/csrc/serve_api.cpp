@@ -253,7 +253,7 @@ attn_status_t attn_kv4_fwd(const void* q, const void* cache, const int32_t* tabl
 
 int64_t attn_window_fwd_workspace(int B, int Hq, int Hkv, int64_t Nq, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Nq < 1 || Nq > kMaxRows ||
-      (d != 64 && d != 128) || too_many(B, Hq, 1 << 30) || !osx::window_is_token(Hq, Hkv, Nq))
+      (d != 64 && d != 128) || too_many(B, Hq, 1 << 30) || !osx::window_is_token(B, Hq, Hkv, Nq))
     return 0;
   return osx::token_workspace(B, Hkv, (int)(Hq / Hkv * Nq), d).bytes;
 }

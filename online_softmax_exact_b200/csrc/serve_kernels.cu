@@ -219,7 +219,7 @@ int launch_window(const WindowLaunch& a, cudaStream_t stream) {
   DeviceProps dp;
   int rc = device_props(&dp);
   if (rc != ATTN_OK) return rc;
-  if (window_is_token(a.Hq, a.Hkv, a.Nq)) {
+  if (window_is_token(a.B, a.Hq, a.Hkv, a.Nq)) {
     const bool few = a.Hq / a.Hkv * a.Nq <= 4;
     if (a.d == 128)
       return few ? launch_token_dn<128, 1>(a, dp, stream) : launch_token_dn<128, 2>(a, dp, stream);
@@ -228,7 +228,19 @@ int launch_window(const WindowLaunch& a, cudaStream_t stream) {
   return a.d == 128 ? launch_window_d<128>(a, dp, stream) : launch_window_d<64>(a, dp, stream);
 }
 
-bool window_is_token(int Hq, int Hkv, long long Nq) { return Hq / Hkv * Nq <= kTokenMaxRows; }
+// The token form costs about 1.45 ns per 16-key block of a unit (8 query rows of a key/value
+// head), the tile form about 1.95 us per 128-key tile and round of 256-row units over the
+// SMs: the token form is the cheaper one up to some 168 units a round. Measured (us, token /
+// tile form; window 4096 and d = 128 unless said): 1 x 8/1 heads, 1 row 10 / 62, 32 rows 21 /
+// 64; 8 x 32/8 heads, 2 rows 42 / 129, 8 rows 101 / 129, 16 rows 192 / 129; 16 x 16/16, d =
+// 64, window 2048, 4 rows 30 / 61, 16 rows 80 / 62; 4 x 32/8, window 128, 16 rows 18 / 12.
+bool window_is_token(int B, int Hq, int Hkv, long long Nq) {
+  constexpr long long kSms = 148, kUnitsPerRound = 160;
+  const long long rows = Hq / Hkv * Nq;
+  const long long units = (long long)B * Hkv * ((rows + 7) / 8);
+  const long long rounds = ((long long)B * Hq * ((Nq + 255) / 256) + kSms - 1) / kSms;
+  return units <= kUnitsPerRound * rounds;
+}
 
 TokenWorkspace token_workspace(int B, int Hkv, int rows, int d) {
   const int tile = rows <= 4 ? TokenCfg<1>::kRows : TokenCfg<2>::kRows;

@@ -52,6 +52,24 @@ def test_window(osx, d, N, window, sinks):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,H,B", [(17, 90, 2), (128, 12, 1), (129, 13, 1), (257, 6, 1), (600, 3, 1)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 4), (128, 0), (129, 129), (200, 700),
+                                          (1000, 3)])
+def test_window_tile_form(osx, d, N, H, B, window, sinks):
+    """Sizes that run on 128-row tiles (no workspace); test_window's run in the token form."""
+    assert osx.lib().attn_window_fwd_workspace(B, H, H, N, d) == 0
+    case(osx, N, N, d, window, sinks, B=B, Hq=H, Hkv=H)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq,Nkv,B,Hq,Hkv", [(70, 500, 4, 8, 2), (300, 900, 1, 8, 8), (300, 300, 2, 5, 5)])
+@pytest.mark.parametrize("window,sinks", [(200, 4), (33, 0), (5000, 1), (150, 300)])
+def test_window_tile_form_newest_rows(osx, d, Nq, Nkv, B, Hq, Hkv, window, sinks):
+    assert osx.lib().attn_window_fwd_workspace(B, Hq, Hkv, Nq, d) == 0
+    case(osx, Nq, Nkv, d, window, sinks, B=B, Hq=Hq, Hkv=Hkv, o_dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("N,window,sinks", [(2500, 300, 4), (2500, 128, 260), (1537, 1024, 64)])
 def test_window_many_units(osx, d, N, window, sinks):
     case(osx, N, N, d, window, sinks, B=2, Hq=6, Hkv=2, o_dtype=torch.bfloat16)
@@ -73,29 +91,29 @@ def test_window_heads(osx, d, Hq, Hkv, Nq):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("Nq", [2, 300])
+@pytest.mark.parametrize("Nq,H", [(2, 1), (300, 1), (300, 5)])
 @pytest.mark.parametrize("q_off,kv_off", [(0, 0), (0, 100), (350, 0), (1000, 0), (1000, 900),
                                           (10 ** 9, 10 ** 9 - 100), (2 ** 40, 0), (500, 200)])
-def test_window_chunk_offsets(osx, d, Nq, q_off, kv_off):
+def test_window_chunk_offsets(osx, d, Nq, H, q_off, kv_off):
     """Chunks before, around and behind the rows' windows, sinks inside and outside the
     chunk: rows without a key are zero with LSE -inf."""
-    case(osx, Nq, 333, d, 120, 230, q_off=q_off, kv_off=kv_off)
-    case(osx, Nq, 333, d, 120, 0, q_off=q_off, kv_off=kv_off)
+    case(osx, Nq, 333, d, 120, 230, q_off=q_off, kv_off=kv_off, Hq=H, Hkv=H)
+    case(osx, Nq, 333, d, 120, 0, q_off=q_off, kv_off=kv_off, Hq=H, Hkv=H)
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("Nq", [1, 100])
-def test_window_inside_a_longer_buffer(osx, d, Nq):
+@pytest.mark.parametrize("Nq,Hkv", [(1, 2), (100, 2), (100, 8)])
+def test_window_inside_a_longer_buffer(osx, d, Nq, Hkv):
     """Keys behind kv_len are never read (they hold NaN here)."""
-    case(osx, Nq, 700, d, 90, 4, B=2, Hq=4, Hkv=2, kv_len=301)
-    case(osx, Nq, 700, d, 1000, 4, B=2, Hq=4, Hkv=2, kv_len=512)
+    case(osx, Nq, 700, d, 90, 4, B=2, Hq=8, Hkv=Hkv, kv_len=301)
+    case(osx, Nq, 700, d, 1000, 4, B=2, Hq=8, Hkv=Hkv, kv_len=512)
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("Nq", [1, 260])
+@pytest.mark.parametrize("Nq,H", [(1, 1), (260, 6)])
 @pytest.mark.parametrize("qsize,scale", [(16.0, None), (1.0, 2.0), (1.0, 1e-6)])
-def test_window_large_and_flat_scores(osx, d, Nq, qsize, scale):
-    case(osx, Nq, 500, d, 180, 4, qsize=qsize, scale=scale)
+def test_window_large_and_flat_scores(osx, d, Nq, H, qsize, scale):
+    case(osx, Nq, 500, d, 180, 4, qsize=qsize, scale=scale, Hq=H, Hkv=H)
 
 
 def test_window_covers_a_causal_call(osx):
