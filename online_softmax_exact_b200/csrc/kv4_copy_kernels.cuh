@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_append_kernel(const Kv
   const int* slots = p.slots + (long long)b * p.N;
   const long long limit = (long long)p.n_pages * p.page_size;
   // the window's first token: aligned with the cache's blocks if slots run on from the first
-  const int s_first = slots[0];
+  // (fewer tokens than a block has fill none, and need not wait for the first slot)
+  const int s_first = p.N < 16 ? 0 : slots[0];
   const int i0 = c * 16 - (s_first > 0 ? s_first % 16 : 0);
   auto slot_of = [&](int row) {
     const int i = i0 + row;
@@ -82,15 +83,17 @@ __global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_append_kernel(const Kv
                                 : __ldcs(reinterpret_cast<const uint4*>(
                                       src + (8 * r + g) * D + 32 * i + 8 * t));
     }
-    uint32_t word[2][L::kGroups], par[2][L::kGroups];
+    uint32_t word[2][L::kGroups] = {}, par[2][L::kGroups] = {};
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2; ++r) {
+      if (!__any_sync(0xffffffffu, slot[r] >= 0)) continue;
 #pragma unroll
       for (int i = 0; i < L::kGroups; ++i) {
         float lo, range;
         group_range<1>(raw[r][i], &lo, &range);
         word[r][i] = quant8(raw[r][i], lo, range, &par[r][i]);
       }
+    }
     if (whole) {
       uint32_t* blk = block_of(base);
       if constexpr (D == 128) {
@@ -134,15 +137,17 @@ __global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_append_kernel(const Kv
                                    : __ldcs(reinterpret_cast<const uint4*>(src + row * D +
                                                                            64 * h2 + 8 * g));
     }
-    uint32_t word[4][D / 64], par[4][D / 64];
+    uint32_t word[4][D / 64] = {}, par[4][D / 64] = {};
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
+    for (int kk = 0; kk < 4; ++kk) {
+      if (!__any_sync(0xffffffffu, slot[kk] >= 0)) continue;
 #pragma unroll
       for (int h2 = 0; h2 < D / 64; ++h2) {
         float lo, range;
         group_range<4>(raw[kk][h2], &lo, &range);
         word[kk][h2] = transpose_nibbles<2>(quant8(raw[kk][h2], lo, range, &par[kk][h2]), g);
       }
+    }
     // parameters: lanes g = 0 and 4 of a group's four
     if (whole) {
       uint32_t* blk = block_of(base);

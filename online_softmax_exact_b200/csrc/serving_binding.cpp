@@ -77,6 +77,19 @@ at::Tensor fresh(at::IntArrayRef shape, ScalarType type, c10::Device dev) {
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 
+// A piece of a buffer as a tensor of its own: several small outputs of one allocation (an
+// allocation costs more than all the rest of a small call's marshalling).
+at::Tensor piece(const at::Tensor& buf, int64_t* at, at::IntArrayRef shape) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW,
+                                                         c10::Storage(buf.storage()), buf.key_set(),
+                                                         buf.dtype());
+  c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+  impl->set_storage_offset(*at);
+  impl->set_sizes_contiguous(shape);
+  *at += c10::multiply_integers(shape);
+  return t;
+}
+
 // The given output, checked, or a new one.
 at::Tensor output(PyObject* o, at::IntArrayRef shape, ScalarType type, c10::Device dev,
                   const char* name) {
@@ -185,9 +198,10 @@ OSX_ENTRY(kv_plan, 8)
       address(free_pages, ScalarType::Int, free_pages.sizes(), dev, "free_pages"));
   const auto* head_p = static_cast<int32_t*>(address(a[4], ScalarType::Int, {1}, dev, "free_head"));
   const c10::cuda::OptionalCUDAGuard guard(dev);
-  at::Tensor slots = fresh({B, n_new}, ScalarType::Int, dev), pos = fresh({B, n_new}, ScalarType::Int, dev);
-  at::Tensor out = fresh({B}, ScalarType::Int, dev), head = fresh({1}, ScalarType::Int, dev);
-  at::Tensor served = fresh({B}, ScalarType::Int, dev);
+  const at::Tensor buf = fresh({2 * B * n_new + 2 * B + 1}, ScalarType::Int, dev);
+  int64_t at = 0;
+  at::Tensor slots = piece(buf, &at, {B, n_new}), pos = piece(buf, &at, {B, n_new});
+  at::Tensor out = piece(buf, &at, {B}), served = piece(buf, &at, {B}), head = piece(buf, &at, {1});
   // an empty list has no address of its own
   check(attn_kv_plan(lens_p, new_p, table_p, free_p ? free_p : lens_p, head_p,
                      static_cast<int32_t*>(slots.data_ptr()), static_cast<int32_t*>(pos.data_ptr()),
