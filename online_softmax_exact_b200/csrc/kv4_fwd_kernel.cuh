@@ -126,6 +126,11 @@ __device__ __forceinline__ int quotient(int a, int n, uint32_t magic) {
   return q + (a - q * n >= n ? 1 : 0);
 }
 
+// Stages of n blocks: 2^stage_shift blocks each.
+__device__ __forceinline__ int kv4_stages(const Kv4FwdParams& p, int n) {
+  return (n + (1 << p.stage_shift) - 1) >> p.stage_shift;
+}
+
 // A place in the stages: unit = (b Hkv + h) row_tiles + rt, and a stage of it.
 struct Kv4Cursor {
   int unit, stage, n_stages;
@@ -133,10 +138,9 @@ struct Kv4Cursor {
   Kv4Span s;
 };
 
-template <int kSB>
 __device__ __forceinline__ void kv4_enter(const Kv4FwdParams& p, Kv4Cursor& c) {
   c.s = kv4_span(p, c.b);
-  c.n_stages = (c.s.n_blocks + kSB - 1) / kSB;
+  c.n_stages = kv4_stages(p, c.s.n_blocks);
 }
 
 // Inclusive prefix sums over the block's threads; *total gets the sum. scan: [kWarps] words.
@@ -192,7 +196,7 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
   const int per_b = p.Hkv * p.row_tiles;  // units of a request
   const int warps = gridDim.x * C::kWarps;
   auto stages_of = [&](int bb) {  // of all of request bb's units
-    return bb < p.B ? (long long)((kv4_span(p, bb).n_blocks + C::kSB - 1) / C::kSB) * per_b : 0ll;
+    return bb < p.B ? (long long)kv4_stages(p, kv4_span(p, bb).n_blocks) * per_b : 0ll;
   };
   long long total = 0, t0 = 0, t1 = 0, pre = 0;
   int b = 0;
@@ -266,7 +270,7 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
   {
     Kv4Cursor c;
     c.b = b;
-    kv4_enter<C::kSB>(p, c);
+    kv4_enter(p, c);
     const int in_b = (int)divide(t0 - pre, c.n_stages);  // unit within the request
     c.stage = (int)((t0 - pre) - (long long)in_b * c.n_stages);
     c.h = in_b / p.row_tiles;
@@ -288,7 +292,7 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
         c.h = 0;
         do {  // the next request that has a stage
           ++c.b;
-          kv4_enter<C::kSB>(p, c);
+          kv4_enter(p, c);
           if (c.n_stages == 0) c.unit += per_b;
         } while (c.n_stages == 0 && c.b + 1 < p.B);
       }
@@ -298,12 +302,12 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
     __syncwarp();
   };
 
-  // ---- this lane's page of the fetch cursor's stage (lanes below kSB), -1: none
+  // ---- this lane's page of the fetch cursor's stage (a lane per block), -1: none
   int page_next = -1, in_page = 0;
   auto look_up = [&](int stage) {
-    const int bi = stage * C::kSB + lane;
+    const int bi = (stage << p.stage_shift) + lane;
     page_next = -1;
-    if (lane < C::kSB && bi < fet.s.n_blocks) {
+    if (lane < 1 << p.stage_shift && bi < fet.s.n_blocks) {
       const int lb = fet.s.block(bi);
       const int pg = quotient(lb, p.blocks_per_page, p.page_magic);
       in_page = lb - pg * p.blocks_per_page;
@@ -430,8 +434,8 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
       const int b_lo = (all_lo + 15) / 16, b_hi = (all_hi + 1) / 16;  // whole blocks
       const int i_lo = sp.n_s + (b_lo > sp.w0 ? b_lo - sp.w0 : 0);  // places in the unit's list
       const int i_hi = sp.n_s + b_hi - sp.w0;
-      in_lo = (i_lo + C::kSB - 1) / C::kSB;
-      in_hi = i_hi > 0 ? i_hi / C::kSB : 0;
+      in_lo = kv4_stages(p, i_lo);
+      in_hi = i_hi > 0 ? i_hi >> p.stage_shift : 0;
     }
 
     // columns 2t and 2t + 1 (high and low parts) of channels 16 mt + g and 16 mt + 8 + g
@@ -517,7 +521,7 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
             }
           }
           if constexpr (kEdge) {
-            const int k0 = cur.s.block(st * C::kSB + j) * 16;
+            const int k0 = cur.s.block((st << p.stage_shift) + j) * 16;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const long long pos = cur.s.p0 + (row0 + nt * 4 + t) % p.Nq;
@@ -595,7 +599,7 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
           }
           if constexpr (kEdge) {
             // rows past the request's length may hold any bits: 0 * NaN is not 0
-            const int k0 = cur.s.block(st * C::kSB + j) * 16;
+            const int k0 = cur.s.block((st << p.stage_shift) + j) * 16;
 #pragma unroll
             for (int r = 0; r < 2; ++r)
               if (k0 + 8 * r + g >= cur.s.len)

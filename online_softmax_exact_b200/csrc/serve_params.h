@@ -67,6 +67,7 @@ struct Kv4FwdParams {
   int blocks_per_page, n_pages, width;
   uint32_t page_magic;      // floor(2^32 / blocks_per_page), 2^32 - 1 for one
   int window, sinks;
+  int stage_shift;          // a stage has 2^stage_shift blocks
   float scale_log2;
 };
 
