@@ -74,7 +74,7 @@ def norm_rope(x, w, inv_freq, pos, eps, interleaved):
 # ------------------------------------------------------------------------------ 4-bit cache
 def quantise(x):
     """bf16 values [..., d] (fp64) -> codes [..., d], scale, zero [..., d / 32] (fp64)."""
-    g = x.reshape(*x.shape[:-1], -1, 32)
+    g = x.reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
     lo, hi = g.min(-1) + 0.0, g.max(-1)  # a zero point of -0 is +0
     scale = bf16((hi - lo) / 15)
     with np.errstate(divide="ignore", invalid="ignore"):
