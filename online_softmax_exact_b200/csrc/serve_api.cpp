@@ -62,7 +62,7 @@ attn_status_t attn_kv_plan(const int32_t* lens, const int32_t* new_lens, int32_t
                          slots, positions, lens_out, head_out,   served};
   for (const void* p : all)
     if (!aligned(p, 4)) return ATTN_ERR_INVALID_ARG;
-  if (too_many(B, n_new, INT32_MAX) || too_many(width, page_size, INT32_MAX))
+  if (too_many(B, n_new, 1 << 30) || too_many(width, page_size, INT32_MAX))
     return ATTN_ERR_UNSUPPORTED;
   const uint64_t b4 = (uint64_t)B * 4;
   const Span in[4] = {span(lens, b4), span(new_lens, b4), span(free_pages, (uint64_t)n_free * 4),
@@ -95,7 +95,7 @@ attn_status_t attn_qk_norm_rope(const void* qkv, int64_t stride_b, int64_t strid
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (n_freq < 1 || 2 * (int64_t)n_freq > d) return ATTN_ERR_INVALID_ARG;
   if (n_freq % 8 != 0) return ATTN_ERR_UNSUPPORTED;
-  if (too_many(B, N, INT32_MAX) || (int64_t)Hq + 2 * (int64_t)Hkv > (1 << 20))
+  if (too_many(B, N, 1 << 30) || (int64_t)Hq + 2 * (int64_t)Hkv > (1 << 20))
     return ATTN_ERR_UNSUPPORTED;
   const int64_t row = ((int64_t)Hq + 2 * (int64_t)Hkv) * d;
   if (stride_b < 0 || stride_n < 0 || stride_b % 8 != 0 || stride_n % 8 != 0 ||
@@ -125,7 +125,7 @@ attn_status_t attn_kv4_append(const void* k, const void* v, void* cache, const i
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return ATTN_ERR_INVALID_ARG;
   const attn_status_t st = check_cache(cache, Hkv, d, page_size, n_pages);
   if (st != ATTN_OK) return st;
-  if (too_many(B, N, INT32_MAX)) return ATTN_ERR_UNSUPPORTED;
+  if (too_many(B, N, 1 << 30)) return ATTN_ERR_UNSUPPORTED;
   const uint64_t bytes = (uint64_t)B * Hkv * N * d * 2;
   const Span in[3] = {span(k, bytes), span(v, bytes), span(slots, (uint64_t)B * N * 4)};
   const Span out[1] = {span(cache, cache_bytes(Hkv, d, page_size, n_pages))};
@@ -157,7 +157,7 @@ attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32
     return ATTN_ERR_INVALID_ARG;
   const attn_status_t st = check_cache(cache, Hkv, d, page_size, n_pages);
   if (st != ATTN_OK) return st;
-  if (too_many(B, N, INT32_MAX) || too_many(width, page_size, INT32_MAX))
+  if (too_many(B, N, 1 << 30) || too_many(width, page_size, INT32_MAX))
     return ATTN_ERR_UNSUPPORTED;
   const uint64_t bytes = (uint64_t)B * Hkv * N * d * 2;
   const Span in[4] = {span(cache, cache_bytes(Hkv, d, page_size, n_pages)),

@@ -141,7 +141,8 @@ def step(osx, s):
                                                       s["head"], page_size=16, n_new=2)
     q, k, v = osx.attn_qk_norm_rope(s["qkv"], s["w"], s["w"], s["inv"], pos, n_heads=8, n_kv_heads=2)
     osx.attn_kv4_append(k, v, s["cache"], slots)
-    o, lse = osx.attn_kv4_fwd(q, s["cache"], s["table"], lens, q_pos=s["lens"], window=200, sinks=4)
+    first = s["lens"].clone()  # (a copy between the launches)
+    o, lse = osx.attn_kv4_fwd(q, s["cache"], s["table"], lens, q_pos=first, window=200, sinks=4)
     ck, cv = osx.attn_kv4_read(s["cache"], s["table"], s["lens"], lens, n=3)
     o2, lse2 = osx.attn_window_fwd(q, s["bk"], s["bv"], window=90, sinks=4)
     o3, lse3 = osx.attn_merge([o, o2], [lse, lse2])
@@ -252,6 +253,46 @@ def test_launches_are_counted(osx):
     step(osx, s)
     # plan, norms, append, attention and its join, read, windowed attention and its join, merge
     assert osx.attn_launch_count() - n == 9
+
+
+def test_offsets_beyond_32_bits(osx):
+    """Pages more than 8 GB into a cache, and key rows more than 4 GB into a tensor."""
+    d, Hkv, page = 128, 8, 128
+    n_pages = 60000
+    cache = osx.kv4_cache(n_pages, Hkv, d, page_size=page)
+    assert cache.numel() > 9 << 30
+    pages = [n_pages - 1, 3, n_pages - 20000]
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn((1, Hkv, 300, d), generator=g).bfloat16().cuda() for _ in range(2))
+    pos = np.arange(300)
+    osx.attn_kv4_append(k, v, cache, i32([np.array(pages)[pos // page] * page + pos % page]))
+    table, lens = i32([pages]), i32([300])
+    rk, rv = osx.attn_kv4_read(cache, table, i32([0]), lens, n=300)
+    vals = [su.values(*su.quantise(su.to_np(x)[0])) for x in (k, v)]
+    assert np.array_equal(su.to_np(rk)[0], su.bf16(vals[0]))
+    assert np.array_equal(su.to_np(rv)[0], su.bf16(vals[1]))
+    q = torch.randn((1, Hkv, 1, d), generator=g).bfloat16().cuda()
+    o, lse = osx.attn_kv4_fwd(q, cache, table, lens)
+    for h in range(Hkv):
+        mags = [np.abs(x[h]) + 2 * np.abs(x[h]).max() for x in vals]  # at least scale c + |zero|
+        ref = su.attention(su.to_np(q)[0, h], vals[0][h], vals[1][h], np.ones((1, 300), bool),
+                           np.float64(np.float32(d ** -0.5)), *mags, mags[1], 2.0 ** -14)
+        su.check(su.to_np(o)[0, h], su.to_np(lse)[0, h], ref, f"head {h}")
+    del cache
+
+    n = 17_500_000
+    for H, Nq in ((1, 1), (1, 2000)):  # token form and tiles
+        kk, vv = (torch.zeros((1, H, n, d), dtype=torch.bfloat16).cuda() for _ in range(2))
+        tail = [torch.randn((1, H, 2300, d), generator=g).bfloat16() for _ in range(2)]
+        kk[:, :, -2300:], vv[:, :, -2300:] = tail[0].cuda(), tail[1].cuda()
+        q = torch.randn((1, H, Nq, d), generator=g).bfloat16()
+        o, lse = osx.attn_window_fwd(q.cuda(), kk, vv, window=250)
+        assert (osx.lib().attn_window_fwd_workspace(1, H, H, Nq, d) > 0) == (Nq == 1)
+        see = su.visible(2300 - Nq + np.arange(Nq), np.arange(2300), 250, 0)
+        ref = su.attention(su.to_np(q)[0, 0], su.to_np(tail[0])[0, 0], su.to_np(tail[1])[0, 0], see,
+                           np.float64(np.float32(d ** -0.5)))
+        su.check(su.to_np(o)[0, 0], su.to_np(lse)[0, 0], ref, f"{Nq} rows")
+        del kk, vv
 
 
 # --------------------------------------------------------------------------------- refusals

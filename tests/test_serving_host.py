@@ -91,7 +91,7 @@ INVALID = {
         dict(ws=6 * G + 4), dict(ws_bytes=1 << 16), dict(ws=G), dict(ws=5 * G - 64)]),
 }
 UNSUPPORTED = {
-    "attn_kv_plan": (PLAN, [dict(B=1 << 20, n_new=1 << 12), dict(width=1 << 20, page=1 << 12)]),
+    "attn_kv_plan": (PLAN, [dict(B=1 << 20, n_new=1 << 12), dict(B=(1 << 30) + 1, n_new=1), dict(width=1 << 20, page=1 << 12)]),
     "attn_qk_norm_rope": (ROPE, [dict(d=96), dict(d=256), dict(n_freq=12), dict(n_freq=4),
                                  dict(B=1 << 16, N=1 << 16), dict(Hq=1 << 21)]),
     "attn_kv4_append": (APPEND, [dict(d=96), dict(page=1 << 20, n_pages=1 << 12),
