@@ -615,9 +615,9 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
               for (int r = 0; r < 2; ++r) {
                 const float x = pr[nt][r] * param_scale(par[r][i]);
                 const float high = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-                // both parts cut to their upper 8 bits
-                bp[nt][i][r] =
-                    transpose_b16(__byte_perm(__float_as_uint(x), __float_as_uint(x - high), 0x7632));
+                // (the low part is rounded, not cut: cut ones would all err to one side, and
+                // over a long context the small sums that are left show it)
+                bp[nt][i][r] = transpose_b16(pack_bf16x2(high, x - high));
                 zo[nt][i] = fmaf(pr[nt][r], param_zero(par[r][i]), zo[nt][i]);
               }
             }

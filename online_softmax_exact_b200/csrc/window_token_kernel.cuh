@@ -193,7 +193,7 @@ window_token_kernel(const __grid_constant__ TokenParams p) {
           const float w = ex2_approx(fmaf(sc[nt][x], p.scale_log2, -base));  // 0 where masked
           l[nt] += w;
           const float high = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
-          part[x] = __byte_perm(__float_as_uint(w), __float_as_uint(w - high), 0x7632);
+          part[x] = pack_bf16x2(high, w - high);
         }
         b0[nt] = transpose_b16(part[0]);
         b1[nt] = transpose_b16(part[1]);

@@ -184,14 +184,14 @@ def fwd_case(osx, seed, B, Hq, Hkv, Nq, d, page, lens, window=0, sinks=0, q_pos=
             vc, vs, vz = take(vp)
             kf, vf = su.values(kc, ks, kz), su.values(vc, vs, vz)
             # the kernel sums scale * c and zero apart; the weight of scale * c enters as
-            # two bf16 numbers, each cut (not rounded) to 8 bits: what is left after the
-            # first is below 2^-7 of it, what is left after the second below 2^-7 of that
+            # two bf16 numbers: the upper 8 bits cut off, the rest (below 2^-7 of it)
+            # rounded by at most 2^-8 of itself
             kmag, vmag = su.values(kc, ks, np.abs(kz)), su.values(vc, vs, 0 * vz)
             vfull = su.values(vc, vs, np.abs(vz))
             for x in range(Hq // Hkv):
                 r = h * (Hq // Hkv) + x
                 ref = su.attention(qn[b, r], kf, vf, see, np.float64(np.float32(scale)), kmag,
-                                   vmag, vfull, 2.0 ** -14, o_dtype == torch.bfloat16)
+                                   vmag, vfull, 2.0 ** -15, o_dtype == torch.bfloat16)
                 su.check(on[b, r], ln[b, r], ref, f"request {b} head {r}")
     return o, lse
 
@@ -263,6 +263,29 @@ def test_fwd_large_and_flat_scores(osx, d, qsize, scale):
     fwd_case(osx, 11, 2, 8, 2, 1, d, 32, [700, 45], qsize=qsize, scale=scale)
 
 
+def test_fwd_weights_err_to_neither_side(osx):
+    """Flat weights over many tokens, codes of one size against the zero point that cancels
+    them: what is left is as exact as unbiased roundings leave it. (Each weight's error is at
+    most 2^-15 of it; a bias of half that would move the result by 2^-16 * 15 scale.)"""
+    rng = np.random.default_rng(0)
+    n, page, d = 20480, 64, 128
+    cache, kp, vp = su.random_cache(rng, n // page, 1, page, d)
+    q = torch.randn((1, 4, 1, d), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    table = np.arange(n // page)[None]
+    o, _ = osx.attn_kv4_fwd(q.cuda(), torch.from_numpy(cache).cuda(), i32(table), i32([n]), scale=0.1)
+    k, v = (su.values(*[x.reshape(n, -1) for x in p]) for p in (kp, vp))
+    full = su.values(vp[0].reshape(n, d), vp[1].reshape(n, -1), np.abs(vp[2].reshape(n, -1)))
+    for h in range(4):
+        s = su.to_np(q)[0, h] @ k.T * np.float64(np.float32(0.1))
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        # independent errors of up to 2^-15 add as their squares do: six of their deviations,
+        # and fp32 sums (256 runs of 80 tokens each: 2^-24 of a run's sum, 2^-24 in the join)
+        bound = 6 * 2.0 ** -15 * np.sqrt(p[0] ** 2 @ full ** 2)
+        bound = bound + 2.0 ** -18 * (p[0] @ full)
+        assert (np.abs(su.to_np(o)[0, h, 0] - p[0] @ v) <= bound).all()
+
+
 def test_fwd_shared_pages(osx):
     """Requests may share pages (a common prefix): the same page in several rows, and twice
     in one."""
@@ -284,5 +307,5 @@ def test_fwd_is_deterministic_and_merges(osx):
     a = osx.attn_kv4_fwd(q, cg, table[:, :17].contiguous(), i32([272]))
     b = osx.attn_kv4_fwd(q, cg, table[:, 17:].contiguous(), i32([368]))
     om, lm = osx.attn_merge([a[0], b[0]], [a[1], b[1]])
-    # weights rounded against other bases: 2^-14 each way of scale * c, up to 0.4 * 15
-    assert (om - o).abs().max() <= 2 * 6 * 2.0 ** -14 and (lm - lse).abs().max() <= 1e-4
+    # weights rounded against other bases: 2^-15 each way of scale * c, up to 0.4 * 15
+    assert (om - o).abs().max() <= 2 * 6 * 2.0 ** -15 and (lm - lse).abs().max() <= 1e-4

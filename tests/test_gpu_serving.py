@@ -84,7 +84,7 @@ class Layer:
                 g = h * self.Hkv // self.Hq
                 ref = su.attention(qn[b, h, :rows[b]], self.keys[b][g], self.vals[b][g], see,
                                    np.float64(np.float32(self.d ** -0.5)), self.kz[b][g],
-                                   self.vz[b][g], self.vz[b][g], 2.0 ** -14,
+                                   self.vz[b][g], self.vz[b][g], 2.0 ** -15,
                                    o.dtype == torch.bfloat16)
                 su.check(on[b, h, :rows[b]], ln[b, h, :rows[b]], ref, f"{what}: request {b} head {h}")
 
@@ -276,7 +276,7 @@ def test_offsets_beyond_32_bits(osx):
     for h in range(Hkv):
         mags = [np.abs(x[h]) + 2 * np.abs(x[h]).max() for x in vals]  # at least scale c + |zero|
         ref = su.attention(su.to_np(q)[0, h], vals[0][h], vals[1][h], np.ones((1, 300), bool),
-                           np.float64(np.float32(d ** -0.5)), *mags, mags[1], 2.0 ** -14)
+                           np.float64(np.float32(d ** -0.5)), *mags, mags[1], 2.0 ** -15)
         su.check(su.to_np(o)[0, h], su.to_np(lse)[0, h], ref, f"head {h}")
     del cache
 
