@@ -3,15 +3,17 @@
 //
 // Query row i at position p_i sees the keys at positions <= p_i that are also > p_i - W
 // or < S. The method and the B200 mapping are those of attn_fwd_kernel.cuh (one CTA per
-// SM, work units of 256 query rows as two 128-row tiles, TMA producer, tcgen05 products
+// SM, work units of two 128-row query tiles, TMA producer, tcgen05 products
 // with S, P and O in tensor memory, one softmax thread per row, one division at the end);
 // what differs is which key tiles are visited:
 //   * a unit's list is the 128-key tiles that hold sinks and the tiles of its rows'
-//     windows, each once: about (W + 255) / 128 + 1 tiles however long the sequence is;
-//   * each of the two query tiles skips the tiles of the list that none of its own rows
-//     sees (the list's last window tile for the first query tile, its first for the
-//     second): those would cost a full product and softmax for nothing. At W = 1024 that
-//     leaves 9 of 10 window tiles to each;
+//     windows, each once, however long the sequence is;
+//   * where query heads share key/value heads in even groups, a unit's two query tiles are
+//     the same 128 rows of two heads, so that both see the same key tiles: 9 window tiles
+//     at W = 1024, in 9 steps;
+//   * elsewhere they are 256 rows of one head, and each skips the tiles of the list that none
+//     of its own rows sees (the list's last window tile for the first, its first for the
+//     second): 9 of 10 tiles each, in 10 steps;
 //   * tiles cut by a row's limits (about two of nine) mask element by element, from one
 //     bit mask per row and 32 keys; the scores are then reduced by the same code as in
 //     whole tiles, a masked score being -inf.
@@ -43,7 +45,7 @@ struct WindowTile {
 };
 
 struct WindowUnit {
-  int bh, qp;
+  int head[2], row0[2];  // of the two query tiles: B Hq head and first row
   int n, n_s, w0;  // the unit's list: tiles 0 .. n_s - 1, then w0 ..
   WindowTile t[2];
   __device__ int tile(int j) const { return j < n_s ? j : w0 + j - n_s; }
@@ -89,11 +91,27 @@ __device__ __forceinline__ void window_place(const WindowParams& p, int u, int* 
   }
 }
 
+// Head and first row of the query tiles of unit u (see WindowParams::pair).
+__device__ __forceinline__ void window_tiles(const WindowParams& p, int u, int (&head)[2],
+                                             int (&row0)[2]) {
+  int bh, qp;
+  window_place(p, u, &bh, &qp);
+  if (p.pair) {
+    head[0] = 2 * bh;
+    head[1] = 2 * bh + 1;
+    row0[0] = row0[1] = qp * 128;
+  } else {
+    head[0] = head[1] = bh;
+    row0[0] = qp * 256;
+    row0[1] = qp * 256 + 128;
+  }
+}
+
 __device__ __forceinline__ WindowUnit window_unit(const WindowParams& p, int u) {
   WindowUnit un;
-  window_place(p, u, &un.bh, &un.qp);
-  un.t[0] = window_tile(p, un.qp * 256);
-  un.t[1] = window_tile(p, un.qp * 256 + 128);
+  window_tiles(p, u, un.head, un.row0);
+  un.t[0] = window_tile(p, un.row0[0]);
+  un.t[1] = window_tile(p, un.row0[1]);
   const WindowTile &a = un.t[0], &b = un.t[1];
   const bool wa = a.last >= a.first, wb = b.last >= b.first;
   un.n_s = a.s > b.s ? a.s : b.s;
@@ -171,17 +189,17 @@ attn_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (u >= p.units) break;
           const WindowUnit un = window_unit(p, u);
           if (un.n == 0) continue;
-          const int kvh = (un.bh / p.Hq) * p.Hkv + (un.bh % p.Hq) / p.group;
+          const int kvh = un.head[0] / p.group;  // B Hkv head: groups lie side by side
           {
             // the next unit's Q into L2 (its buffer is free only after this unit's last
             // Q.K^T)
             const int u2 = unit_for_round(r + 1, blockIdx.x, G);
             if (u2 < p.units) {
-              int bh2, qp2;
-              window_place(p, u2, &bh2, &qp2);
+              int head2[2], row2[2];
+              window_tiles(p, u2, head2, row2);
               for (int t = 0; t < 2; ++t)
                 for (int h = 0; h < D / 64; ++h)
-                  tma_prefetch_l2_3d(&tmQ, h * 64, qp2 * 256 + t * 128, bh2);
+                  tma_prefetch_l2_3d(&tmQ, h * 64, row2[t], head2[t]);
             }
           }
           if (!(ok = mbar_wait(bar(B_QE), (qcount & 1) ^ 1, abort_flag, p.status))) break;
@@ -190,7 +208,7 @@ attn_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           for (int t = 0; t < 2; ++t)
             for (int h = 0; h < D / 64; ++h)
               tma_load_3d(sbase + C::kQOff + t * C::kTileBytes + h * 16384, &tmQ, bar(B_QF),
-                          h * 64, un.qp * 256 + t * 128, un.bh);
+                          h * 64, un.row0[t], un.head[t]);
           for (int j = 0; j < un.n; ++j) {
             const int row = un.tile(j) * 128;
             if (!(ok = mbar_wait(bar(B_KE + ks), kph ^ 1, abort_flag, p.status))) break;
@@ -339,8 +357,9 @@ attn_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const int u = unit_for_round(rr, blockIdx.x, G);
       if (u >= p.units) break;
       const WindowUnit un = window_unit(p, u);
-      const WindowTile wt = un.t[t];
-      const int row0 = un.qp * 256 + t * 128;  // first row of this tile
+      const WindowTile wt = t ? un.t[1] : un.t[0];
+      const int row0 = t ? un.row0[1] : un.row0[0];  // first row of this tile
+      const int head = t ? un.head[1] : un.head[0];
       const long long row = (long long)row0 + r;
       float m = -INFINITY, l = 0.f;
 
@@ -446,7 +465,7 @@ attn_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const int wrow0 = row0 + wq * 32;
       const int per = p.o_bf16 ? 64 : 32;  // values of a row's 128 bytes
       const int es = p.o_bf16 ? 2 : 4;
-      char* base = static_cast<char*>(p.o) + ((long long)un.bh * p.Nq + wrow0) * D * es;
+      char* base = static_cast<char*>(p.o) + ((long long)head * p.Nq + wrow0) * D * es;
 #pragma unroll 1
       for (int q4 = 0; q4 < D / per; ++q4) {
         if (wt.any()) {
@@ -490,7 +509,7 @@ attn_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         __syncwarp();  // the buffer is rewritten by the next chunk
       }
       if (row < p.Nq)
-        p.lse[(long long)un.bh * p.Nq + row] =
+        p.lse[(long long)head * p.Nq + row] =
             seen ? (m + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
       tc_fence_before();
     }

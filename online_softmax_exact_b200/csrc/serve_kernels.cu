@@ -206,14 +206,19 @@ int launch_window_d(const WindowLaunch& a, const DeviceProps& dp, cudaStream_t s
   const long long s = a.sinks - a.kv_off;
   p.sinks = (int)(s < 0 ? 0 : (s < a.Nkv ? s : a.Nkv));
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-  p.row_blocks = (int)((a.Nq + 255) / 256);
-  const long long units = (long long)a.B * a.Hq * p.row_blocks;
+  p.pair = p.group % 2 == 0;
+  const int per_block = p.pair ? 128 : 256;
+  p.heads = p.pair ? a.B * a.Hq / 2 : a.B * a.Hq;
+  p.row_blocks = (int)((a.Nq + per_block - 1) / per_block);
+  const long long units = (long long)p.heads * p.row_blocks;
   if (units > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   p.units = (int)units;
-  p.heads = a.B * a.Hq;
-  long long cut = (a.window - 1 - p.rel + 255) / 256;  // 256 qp < window - 1 - rel
-  if (a.window - 1 - p.rel <= 0) cut = 0;
-  p.cut_blocks = (int)(cut < p.row_blocks ? cut : p.row_blocks);
+  // row blocks with per_block qp < window - 1 - rel
+  const long long cut = a.window - 1 - p.rel;
+  p.cut_blocks = (int)(cut <= 0 ? 0
+                                : ((cut + per_block - 1) / per_block < p.row_blocks
+                                       ? (cut + per_block - 1) / per_block
+                                       : p.row_blocks));
   const int rc = prepare_kernel<attn_window_kernel<D>>(C::kSmemBytes, false);
   if (rc != ATTN_OK) return rc;
   const int grid = units < dp.num_sms ? (int)units : dp.num_sms;

@@ -120,7 +120,8 @@ struct WindowParams {
   int Nq, Nkv;
   long long rel;     // position of query row 0 less that of key row 0
   int window, sinks; // sinks: key rows [0, sinks) of this chunk stay visible
-  int heads, row_blocks, units;  // heads: B Hq
+  int pair;        // a unit is 128 rows of two neighbouring heads, else 256 rows of one
+  int heads, row_blocks, units;  // heads (or pairs of them), row blocks of 128 or 256
   int cut_blocks;  // row blocks whose windows the sequence's start cuts
   float scale_log2;
 };

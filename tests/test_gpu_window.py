@@ -53,12 +53,14 @@ def test_window(osx, d, N, window, sinks):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("N,H,B", [(17, 90, 2), (128, 12, 1), (129, 13, 1), (257, 6, 1), (600, 3, 1)])
+@pytest.mark.parametrize("group", [1, 2])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 4), (128, 0), (129, 129), (200, 700),
                                           (1000, 3)])
-def test_window_tile_form(osx, d, N, H, B, window, sinks):
-    """Sizes that run on 128-row tiles (no workspace); test_window's run in the token form."""
-    assert osx.lib().attn_window_fwd_workspace(B, H, H, N, d) == 0
-    case(osx, N, N, d, window, sinks, B=B, Hq=H, Hkv=H)
+def test_window_tile_form(osx, d, N, H, B, group, window, sinks):
+    """Sizes that run on 128-row tiles (no workspace); test_window's run in the token form.
+    Groups of two heads run as pairs of heads, single ones as pairs of row tiles."""
+    assert osx.lib().attn_window_fwd_workspace(B, group * H, H, N, d) == 0
+    case(osx, N, N, d, window, sinks, B=B, Hq=group * H, Hkv=H)
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -71,8 +73,9 @@ def test_window_tile_form_newest_rows(osx, d, Nq, Nkv, B, Hq, Hkv, window, sinks
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("N,window,sinks", [(2500, 300, 4), (2500, 128, 260), (1537, 1024, 64)])
-def test_window_many_units(osx, d, N, window, sinks):
-    case(osx, N, N, d, window, sinks, B=2, Hq=6, Hkv=2, o_dtype=torch.bfloat16)
+@pytest.mark.parametrize("Hq,Hkv", [(6, 2), (8, 2), (5, 5)])
+def test_window_many_units(osx, d, N, window, sinks, Hq, Hkv):
+    case(osx, N, N, d, window, sinks, B=2, Hq=Hq, Hkv=Hkv, o_dtype=torch.bfloat16)
 
 
 @pytest.mark.parametrize("d", [64, 128])
