@@ -105,11 +105,17 @@ __global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_append_kernel(const Kv
         *reinterpret_cast<uint4*>(blk + lane * 4) =
             make_uint4(word[0][0], word[0][1], word[1][0], word[1][1]);
       }
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int i = 0; i < L::kGroups; ++i)
-          if (t == i) blk[L::kKParams + (8 * r + g) * L::kGroups + i] = par[r][i];
+      // a row's parameters are on all of its lanes
+      if (t < 2) {
+        uint32_t* row = blk + L::kKParams + (8 * t + g) * L::kGroups;
+        if constexpr (D == 128)
+          *reinterpret_cast<uint4*>(row) = make_uint4(
+              t ? par[1][0] : par[0][0], t ? par[1][1] : par[0][1], t ? par[1][2] : par[0][2],
+              t ? par[1][3] : par[0][3]);
+        else
+          *reinterpret_cast<uint2*>(row) =
+              make_uint2(t ? par[1][0] : par[0][0], t ? par[1][1] : par[0][1]);
+      }
     } else {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(
     const __grid_constant__ RopeParams p, int split) {
   constexpr int kLanes = D / 8;         // lanes per row
   constexpr int kRows = 32 / kLanes;    // rows of a warp's pass
-  constexpr int kAhead = 4;             // passes in flight
+  constexpr int kAhead = 3;             // passes in flight (2: 167 us, 3: 140, 4: 146, 6: 149)
   constexpr int kWarps = kRopeThreads / 32;
   __shared__ __align__(16) float s_cos[kWarps][D / 2], s_sin[kWarps][D / 2];
   __shared__ __align__(16) float s_w[2][D];
