@@ -18,6 +18,9 @@
 //     bit mask per row and 32 keys; the scores are then reduced by the same code as in
 //     whole tiles, a masked score being -inf.
 // Bound: as in attn_fwd_kernel the tensor core and the exponentials of the visited tiles.
+// Measured: 32 768 rows, 32 heads on 8, window 1024, 64 sinks: 657 us in a short run (1.05
+// PFLOP/s of visited tiles), 753 us under the power cap; pairs of row tiles of one head took
+// 707. 2 x 16 heads of 4001 rows: 91 and 98 us.
 //
 // The K/V tensor maps end with the chunk, so rows past it read as zero. A key row inside
 // the chunk that some row of a visited tile does not see still enters that row's product

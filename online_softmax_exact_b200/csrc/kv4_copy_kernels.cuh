@@ -7,6 +7,9 @@
 // (values) bytes of a row. Windows are cut where the cache's blocks are, so in a prompt
 // all but the first and last of a request's windows fill a block exactly; the others
 // (and single tokens) store word by word.
+// Measured (24.6k tokens of 8 heads, d = 128): append 42 us (131 MB, 3.1 TB/s: bound by the
+// instructions of the quantisation), read 34 us (165 MB, 4.9 TB/s). Plain divisions and
+// slots resolved value by value took 65 us.
 #pragma once
 
 #include <cuda_bf16.h>

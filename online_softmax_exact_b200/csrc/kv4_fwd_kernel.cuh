@@ -41,6 +41,10 @@
 //     results do not depend on timing). A unit that lies within one warp's run is finished
 //     there. Warp w's partial of unit u has slot w + u: both only grow along the stages.
 // Statistics and sums are fp32.
+// Measured (32 query heads on 8, d = 128): 131 072 tokens 40 us (168 MB, 4.2 TB/s with start
+// and join; the fetches alone, with start and join, 33 us); 32 requests of up to 8 192
+// tokens 54 us (224 MB; fetches alone 46 us). Codes as 128 + c with the bias taken out
+// again: 570 warp instructions per block of 16 tokens, and as subnormals 330.
 //
 // Pages are looked up in the table and checked against n_pages: keys on a page outside
 // the cache are invisible. Rows of a page past a request's length may hold anything.

@@ -18,6 +18,10 @@
 // lines), so a rotation needs no exchange between lanes; arithmetic is in packed fp32
 // pairs.
 //
+// Measured: 32 768 tokens of 32 + 2 * 8 heads, d = 128 (805 MB): 140 us in a short run, 145
+// us under power, 5.6 TB/s; a block per token with whole-block barriers took 190. One token
+// of 32 requests: 4.1 us.
+//
 // Angles: position * inv_freq in 64 bits, reduced to [-pi, pi] in 64 bits, and only then
 // sine and cosine in fp32. An fp32 product would be off by 2^-24 of an angle of up to
 // 10^5 radians, several times the bf16 spacing of the result.
