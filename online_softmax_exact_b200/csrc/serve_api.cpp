@@ -209,6 +209,10 @@ attn_status_t attn_kv4_fwd(const void* q, const void* cache, const int32_t* tabl
   if (too_many(B, Hq, 1 << 30) || too_many(Hq, Nq, 1 << 30) ||
       too_many(width, page_size, INT32_MAX))
     return ATTN_ERR_UNSUPPORTED;
+  // blocks of 16 tokens over all query tiles: a warp's share has to fit 31 bits
+  const int64_t tiles = (int64_t)B * Hkv * (((int64_t)Hq / Hkv * Nq + 3) / 4);
+  if (too_many(tiles, ((int64_t)width * page_size + 15) / 16, int64_t(1) << 40))
+    return ATTN_ERR_UNSUPPORTED;
   const uint64_t rows = (uint64_t)B * Hq * Nq;
   const Span in[5] = {span(q, rows * d * 2), span(cache, cache_bytes(Hkv, d, page_size, n_pages)),
                       span(table, (uint64_t)B * width * 4), span(lens, (uint64_t)B * 4),

@@ -137,17 +137,18 @@ def token_words(d):
             for t in range(16)}
 
 
-def random_cache(rng, n_pages, Hkv, page, d):
-    """A cache of random codes and sensible parameters, and what it stands for:
-    cache uint8, and per (k, v) codes [n_pages, Hkv, page, d], scale, zero [.., d / 32]."""
+def random_cache(rng, n_pages, Hkv, page, d, ksize=1.0, vsize=1.0):
+    """A cache of random codes and sensible parameters (times a power of two), and what it
+    stands for: cache uint8, and per (k, v) codes [n_pages, Hkv, page, d], scale, zero [.., d / 32]."""
     blocks = page // 16
     cache = np.zeros((n_pages, Hkv, blocks, 20 * d), np.uint8)
     words = cache.view(np.uint32)
     parts = []
     for which in ("k", "v"):
         c = rng.integers(0, 16, (n_pages, Hkv, blocks, 16, d))
-        s = bf16(rng.uniform(0.05, 0.4, (n_pages, Hkv, blocks, 16, d // 32)))
-        z = bf16(rng.uniform(-3, 0.2, s.shape))
+        size = ksize if which == "k" else vsize
+        s = bf16(rng.uniform(0.05, 0.4, (n_pages, Hkv, blocks, 16, d // 32))) * size
+        z = bf16(rng.uniform(-3, 0.2, s.shape)) * size
         e = np.arange(d)
         for t in range(16):
             w, n = zip(*(word_of(which, t, x, d) for x in e))

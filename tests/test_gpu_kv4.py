@@ -136,13 +136,14 @@ def test_read_past_the_table(osx):
 
 # --------------------------------------------------------------------------------- forward
 def fwd_case(osx, seed, B, Hq, Hkv, Nq, d, page, lens, window=0, sinks=0, q_pos=None, scale=None,
-             o_dtype=torch.float32, qsize=1.0, max_len=0, bad_pages=(), width=None, table=None):
+             o_dtype=torch.float32, qsize=1.0, max_len=0, bad_pages=(), width=None, table=None,
+             ksize=1.0, vsize=1.0):
     rng = np.random.default_rng(seed)
     lens = np.asarray(lens)
     if width is None:
         width = max(1, int(-(-max(int(lens.max()), 1) // page)))
     n_pages = B * width + 2
-    cache, kp, vp = su.random_cache(rng, n_pages, Hkv, page, d)
+    cache, kp, vp = su.random_cache(rng, n_pages, Hkv, page, d, ksize, vsize)
     if table is None:
         table = rng.permutation(n_pages)[:B * width].reshape(B, width)
     for b, p, x in bad_pages:
@@ -284,6 +285,16 @@ def test_fwd_weights_err_to_neither_side(osx):
         bound = 6 * 2.0 ** -15 * np.sqrt(p[0] ** 2 @ full ** 2)
         bound = bound + 2.0 ** -18 * (p[0] @ full)
         assert (np.abs(su.to_np(o)[0, h, 0] - p[0] @ v) <= bound).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("qsize,ksize,vsize", [
+    (1.0, 1.0, 2.0 ** -35), (1.0, 1.0, 2.0 ** 21), (2.0 ** 90, 2.0 ** -90, 1.0),
+    (2.0 ** -60, 2.0 ** 60, 1.0), (2.0 ** 20, 2.0 ** -18, 2.0 ** 10), (2.0 ** -110, 1.0, 1.0)])
+def test_fwd_sizes_of_values(osx, d, qsize, ksize, vsize):
+    """Queries, keys and values of any size: their operands carry powers of two."""
+    fwd_case(osx, 14, 2, 8, 2, 1, d, 16, [300, 41], qsize=qsize, ksize=ksize, vsize=vsize)
+    fwd_case(osx, 14, 2, 8, 2, 2, d, 16, [300, 41], qsize=qsize, ksize=ksize, vsize=vsize)
 
 
 def test_fwd_shared_pages(osx):

@@ -138,3 +138,32 @@ def test_window_partials_merge(osx, Nq):
     o, lse = osx.attn_merge([p[0] for p in parts], [p[1] for p in parts])
     assert (o - whole[0]).abs().max() <= 2 * 5 * su.HALF_BF16
     assert (lse - whole[1]).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq,H", [(3, 2), (200, 8)])
+def test_window_of_parent_rows(osx, d, Nq, H):
+    """The C entry point on rows inside longer parents (q_ld, kv_ld), chunk starts included;
+    parent rows outside hold NaN."""
+    B, q_ld, kv_ld, q0, k0, Nkv = 2, 300, 500, 31, 77, 380
+    q = torch.full((B, H, q_ld, d), float("nan"), dtype=torch.bfloat16)
+    k, v = (torch.full((B, H, kv_ld, d), float("nan"), dtype=torch.bfloat16) for _ in range(2))
+    q[:, :, q0:q0 + Nq] = randn_bf16((B, H, Nq, d), 6, 0)
+    k[:, :, k0:k0 + Nkv], v[:, :, k0:k0 + Nkv] = (randn_bf16((B, H, Nkv, d), 6, i) for i in (1, 2))
+    qg, kg, vg = q.cuda(), k.cuda(), v.cuda()
+    o = torch.empty((B, H, Nq, d), device="cuda")
+    lse = torch.empty((B, H, Nq), device="cuda")
+    lib = osx.lib()
+    n = lib.attn_window_fwd_workspace(B, H, H, Nq, d)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+    st = lib.attn_window_fwd(qg.data_ptr() + q0 * d * 2, kg.data_ptr() + k0 * d * 2,
+                             vg.data_ptr() + k0 * d * 2, o.data_ptr(), lse.data_ptr(), 0, B, H, H, Nq,
+                             Nkv, q_ld, kv_ld, 190, 0, d, 100, 3, d ** -0.5, ws.data_ptr(), n,
+                             torch.cuda.current_stream().cuda_stream)
+    assert st == osx.ATTN_OK and osx.attn_device_status() == osx.ATTN_OK
+    see = su.visible(190 + np.arange(Nq), np.arange(Nkv), 100, 3)
+    for b in range(B):
+        for h in range(H):
+            ref = su.attention(su.to_np(q)[b, h, q0:q0 + Nq], su.to_np(k)[b, h, k0:k0 + Nkv],
+                               su.to_np(v)[b, h, k0:k0 + Nkv], see, np.float64(np.float32(d ** -0.5)))
+            su.check(su.to_np(o)[b, h], su.to_np(lse)[b, h], ref, f"batch {b} head {h}")

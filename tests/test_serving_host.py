@@ -99,7 +99,8 @@ UNSUPPORTED = {
     "attn_kv4_read": (READ, [dict(d=32), dict(page=1 << 20, n_pages=1 << 12),
                              dict(B=1 << 16, N=1 << 16), dict(width=1 << 28)]),
     "attn_kv4_fwd": (KV4, [dict(d=256), dict(page=1 << 20, n_pages=1 << 12), dict(width=1 << 28),
-                           dict(B=1 << 20, Hq=1 << 12), dict(Nq=1 << 30)]),
+                           dict(B=1 << 20, Hq=1 << 12), dict(Nq=1 << 30),
+                           dict(B=1 << 16, page=1 << 20, n_pages=1, width=1 << 10)]),
     "attn_window_fwd": (WIN, [dict(d=96), dict(Nq=1 << 31, q_ld=1 << 31), dict(kv_ld=1 << 31),
                               dict(q_off=1 << 61), dict(kv_off=1 << 61), dict(B=1 << 20, Hq=1 << 12)]),
 }
