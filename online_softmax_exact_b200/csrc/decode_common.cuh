@@ -33,7 +33,7 @@ __device__ __forceinline__ long long decode_runs(long long total, int warps) {
 
 // Joins the partials of one row of one unit, kHalf of its values: kLanes lanes per partial,
 // the partials dealt to the block's groups of lanes, in two steps whose order does not
-// depend on timing. kThreads: 128, or 512 where a unit has many partials.
+// depend on timing. kThreads goes by the number of partials (launch_join).
 template <int D, int kRows, int kThreads>
 __global__ void __launch_bounds__(kThreads) decode_join_kernel(
     const __grid_constant__ JoinParams p) {

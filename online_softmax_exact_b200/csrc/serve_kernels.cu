@@ -71,15 +71,21 @@ int prepare_kernel(uint32_t smem, bool clusters) {
   return ATTN_OK;
 }
 
-// The join of a decode launch, 64 values of a row to a block. A unit has about
-// warps / units partials.
+// The join of a decode launch, 64 values of a row to a block. A unit has about warps / units
+// partials, and no more than stages; a block takes up to five per group of 16 threads in one
+// round of loads. (Measured with 128 / 256 / 512 threads: 55 partials a unit 18.0 / 17.2 /
+// 18.4 us for the whole call, 148 partials 40.6 / 40.4 / 39.6 us.)
 template <int D, int kRows>
-int launch_join(const JoinParams& j, cudaStream_t stream) {
+int launch_join(const JoinParams& j, long long stages, cudaStream_t stream) {
   const long long units = (long long)j.B * j.Hkv * j.row_tiles;
   const unsigned grid = grid_1d(units * kRows * (D / 64));
   if (!grid) return ATTN_ERR_UNSUPPORTED;
-  if (units * 16 >= j.n_warps)
+  long long parts = j.n_warps / units + 1;
+  if (stages < parts) parts = stages;
+  if (parts <= 40)
     return launch_dependent(decode_join_kernel<D, kRows, 128>, grid, 128, 0, stream, j);
+  if (parts <= 80)
+    return launch_dependent(decode_join_kernel<D, kRows, 256>, grid, 256, 0, stream, j);
   return launch_dependent(decode_join_kernel<D, kRows, 512>, grid, 512, 0, stream, j);
 }
 
@@ -96,14 +102,14 @@ int launch_kv4_fwd_dn(Kv4FwdParams p, long long max_len, int num_sms, cudaStream
   int grid = num_sms < kKv4MaxBlocks ? num_sms : kKv4MaxBlocks;
   // one block to a stage where that gives every warp at most one (a short call's time is
   // that of its longest chain: 3 requests of up to 700 tokens, windowed, 10.2 -> 8.9 us)
-  long long stages = items * (keys / 16 + 2);
+  long long stages = keys / 16 + 2;  // of a unit, at most
   p.stage_shift = 0;
-  if (stages > (long long)grid * C::kWarps) {
-    stages = items * (keys / (16 * C::kSB) + 2);
+  if (items * stages > (long long)grid * C::kWarps) {
+    stages = keys / (16 * C::kSB) + 2;
     p.stage_shift = C::kSB == 4 ? 2 : 1;
   }
   static_assert(C::kSB == 2 || C::kSB == 4, "blocks of a stage");
-  if (stages < grid) grid = (int)stages;
+  if (items * stages < grid) grid = (int)(items * stages);
   const int rc = prepare_kernel<kv4_fwd_kernel<D, NT>>(C::kSmemBytes, false);
   if (rc != ATTN_OK) return rc;
   const int st =
@@ -111,7 +117,7 @@ int launch_kv4_fwd_dn(Kv4FwdParams p, long long max_len, int num_sms, cudaStream
   if (st != ATTN_OK) return st;
   const JoinParams j{p.ws_o, p.ws_ml, p.ws_prefix, 0, p.o, p.lse, p.o_bf16, p.B, p.Hkv, p.rows,
                      p.row_tiles, grid * C::kWarps};
-  return launch_join<D, C::kRows>(j, stream);
+  return launch_join<D, C::kRows>(j, stages, stream);
 }
 
 template <int D, int NT>
@@ -180,7 +186,7 @@ int launch_token_dn(const WindowLaunch& a, const DeviceProps& dp, cudaStream_t s
   }
   const JoinParams j{p.ws_o,   p.ws_ml, nullptr, p.n_blocks, p.o,         p.lse,
                      p.o_bf16, p.B,     p.Hkv,   p.rows,     p.row_tiles, grid * C::kWarps};
-  return launch_join<D, C::kRows>(j, stream);
+  return launch_join<D, C::kRows>(j, p.n_blocks, stream);
 }
 
 template <int D>
