@@ -7,9 +7,10 @@
 // (values) bytes of a row. Windows are cut where the cache's blocks are, so in a prompt
 // all but the first and last of a request's windows fill a block exactly; the others
 // (and single tokens) store word by word.
-// Measured (24.6k tokens of 8 heads, d = 128): append 42 us (131 MB, 3.1 TB/s: bound by the
-// instructions of the quantisation), read 34 us (165 MB, 4.9 TB/s). Plain divisions and
-// slots resolved value by value took 65 us.
+// Measured (24.6k tokens of 8 heads, d = 128): append 46 us (131 MB, 2.8 TB/s: instructions
+// issue in 63% of the cycles, and 32 warps an SM do not hide all of the loads' latency), read
+// 35 us (165 MB, 4.7 TB/s), both in a stream, overlapping, 69 us. Plain divisions and
+// slots resolved value by value took half as long again, items found in 64-bit divisions 1 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -23,25 +24,30 @@
 
 namespace osx {
 
-constexpr int kKv4CopyWarps = 8;
+// Warps of a block, and blocks of the append kernel kept on an SM: 64 registers a thread. Both
+// kernels on the tokens above, blocks of 8 / 4 / 2 warps: 70.7 / 68.8 / 73.4 us; 8 warps at
+// 72 registers (3 blocks) 75.1 us, at 48 (5 blocks, spilling) 72.8 us.
+constexpr int kKv4CopyWarps = 4;
+constexpr int kKv4AppendBlocks = 8;
 
 // Warp -> (request, window, head, keys or values); neighbouring warps take neighbouring
 // heads of one window. False past the end.
 __device__ __forceinline__ bool kv4_copy_item(const Kv4CopyParams& p, int& b, int& c, int& h,
                                               int& which) {
-  long long w = (long long)blockIdx.x * kKv4CopyWarps + threadIdx.x / 32;
-  if (w >= (long long)p.B * p.windows * p.Hkv * 2) return false;
+  uint32_t w = blockIdx.x * kKv4CopyWarps + threadIdx.x / 32;
+  if (w >= p.items) return false;
   which = (int)(w & 1);
   w >>= 1;
-  h = (int)(w % p.Hkv);
-  w /= p.Hkv;
-  c = (int)(w % p.windows);
-  b = (int)(w / p.windows);
+  const uint32_t q = w / (uint32_t)p.Hkv;
+  h = (int)(w - q * (uint32_t)p.Hkv);
+  b = (int)(q / (uint32_t)p.windows);
+  c = (int)(q - (uint32_t)b * (uint32_t)p.windows);
   return true;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kKv4CopyWarps * 32) kv4_append_kernel(const Kv4CopyParams p) {
+__global__ void __launch_bounds__(kKv4CopyWarps * 32, kKv4AppendBlocks)
+    kv4_append_kernel(const Kv4CopyParams p) {
   using L = Kv4<D>;
   int b, c, h, which;
   if (!kv4_copy_item(p, b, c, h, which)) return;

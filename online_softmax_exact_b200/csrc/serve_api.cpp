@@ -45,6 +45,15 @@ uint64_t cache_bytes(int Hkv, int d, int page_size, int n_pages) {
 
 bool too_many(int64_t a, int64_t b, int64_t limit) { return a > limit / b; }
 
+// Windows of 16 tokens that N tokens can touch, wherever they start, and the copy kernels'
+// items, two per window and head; 0 where they leave 32 bits (over 500 GB of rows).
+int copy_windows(int N) { return (int)(((int64_t)N + 30) / 16); }
+
+unsigned copy_items(int B, int N, int Hkv) {
+  const int64_t per = 2 * (int64_t)copy_windows(N) * Hkv;
+  return too_many(per, B, 0xffffff00LL) ? 0u : (unsigned)(per * B);
+}
+
 }  // namespace
 
 extern "C" {
@@ -125,7 +134,7 @@ attn_status_t attn_kv4_append(const void* k, const void* v, void* cache, const i
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return ATTN_ERR_INVALID_ARG;
   const attn_status_t st = check_cache(cache, Hkv, d, page_size, n_pages);
   if (st != ATTN_OK) return st;
-  if (too_many(B, N, 1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  if (too_many(B, N, 1 << 30) || !copy_items(B, N, Hkv)) return ATTN_ERR_UNSUPPORTED;
   const uint64_t bytes = (uint64_t)B * Hkv * N * d * 2;
   const Span in[3] = {span(k, bytes), span(v, bytes), span(slots, (uint64_t)B * N * 4)};
   const Span out[1] = {span(cache, cache_bytes(Hkv, d, page_size, n_pages))};
@@ -142,7 +151,8 @@ attn_status_t attn_kv4_append(const void* k, const void* v, void* cache, const i
   p.Hkv = Hkv;
   p.page_size = page_size;
   p.n_pages = n_pages;
-  p.windows = (int)(((int64_t)N + 30) / 16);
+  p.windows = copy_windows(N);
+  p.items = copy_items(B, N, Hkv);
   return static_cast<attn_status_t>(
       osx::launch_kv4_append(p, d, static_cast<cudaStream_t>(stream)));
 }
@@ -157,7 +167,7 @@ attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32
     return ATTN_ERR_INVALID_ARG;
   const attn_status_t st = check_cache(cache, Hkv, d, page_size, n_pages);
   if (st != ATTN_OK) return st;
-  if (too_many(B, N, 1 << 30) || too_many(width, page_size, INT32_MAX))
+  if (too_many(B, N, 1 << 30) || too_many(width, page_size, INT32_MAX) || !copy_items(B, N, Hkv))
     return ATTN_ERR_UNSUPPORTED;
   const uint64_t bytes = (uint64_t)B * Hkv * N * d * 2;
   const Span in[4] = {span(cache, cache_bytes(Hkv, d, page_size, n_pages)),
@@ -180,7 +190,8 @@ attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32
   p.page_size = page_size;
   p.n_pages = n_pages;
   p.width = width;
-  p.windows = (int)(((int64_t)N + 30) / 16);
+  p.windows = copy_windows(N);
+  p.items = copy_items(B, N, Hkv);
   return static_cast<attn_status_t>(osx::launch_kv4_read(p, d, static_cast<cudaStream_t>(stream)));
 }
 

@@ -297,26 +297,22 @@ int launch_qk_norm_rope(const RopeParams& p, int d, int interleaved, cudaStream_
   return launch_dependent(kernel, grid, kRopeThreads, 0, stream, p, split);
 }
 
-int launch_kv4_append(const Kv4CopyParams& p, int d, cudaStream_t stream) {
+static int launch_kv4_copy(void (*kernel)(Kv4CopyParams), const Kv4CopyParams& p,
+                           cudaStream_t stream) {
   DeviceProps dp;
-  int rc = device_props(&dp);
+  const int rc = device_props(&dp);
   if (rc != ATTN_OK) return rc;
-  const unsigned grid =
-      grid_1d(((long long)p.B * p.windows * p.Hkv * 2 + kKv4CopyWarps - 1) / kKv4CopyWarps);
+  const unsigned grid = grid_1d(((long long)p.items + kKv4CopyWarps - 1) / kKv4CopyWarps);
   if (!grid) return ATTN_ERR_UNSUPPORTED;
-  return launch_dependent(d == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>, grid,
-                          kKv4CopyWarps * 32, 0, stream, p);
+  return launch_dependent(kernel, grid, kKv4CopyWarps * 32, 0, stream, p);
+}
+
+int launch_kv4_append(const Kv4CopyParams& p, int d, cudaStream_t stream) {
+  return launch_kv4_copy(d == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>, p, stream);
 }
 
 int launch_kv4_read(const Kv4CopyParams& p, int d, cudaStream_t stream) {
-  DeviceProps dp;
-  int rc = device_props(&dp);
-  if (rc != ATTN_OK) return rc;
-  const unsigned grid =
-      grid_1d(((long long)p.B * p.windows * p.Hkv * 2 + kKv4CopyWarps - 1) / kKv4CopyWarps);
-  if (!grid) return ATTN_ERR_UNSUPPORTED;
-  return launch_dependent(d == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>, grid,
-                          kKv4CopyWarps * 32, 0, stream, p);
+  return launch_kv4_copy(d == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>, p, stream);
 }
 
 // 4 query rows a unit, or 8 (the unpacked codes then serve twice the rows)

@@ -48,6 +48,7 @@ struct Kv4CopyParams {
   const int* start;         // read: [B]
   const int* lens;          // read: [B]
   int B, N, Hkv, page_size, n_pages, width, windows;
+  unsigned items;  // a warp each: (request, window, head, keys or values)
 };
 
 struct Kv4FwdParams {

@@ -95,9 +95,10 @@ UNSUPPORTED = {
     "attn_qk_norm_rope": (ROPE, [dict(d=96), dict(d=256), dict(n_freq=12), dict(n_freq=4),
                                  dict(B=1 << 16, N=1 << 16), dict(Hq=1 << 21)]),
     "attn_kv4_append": (APPEND, [dict(d=96), dict(page=1 << 20, n_pages=1 << 12),
-                                 dict(B=1 << 16, N=1 << 16)]),
+                                 dict(B=1 << 16, N=1 << 16), dict(N=1 << 29, Hkv=64, n_pages=1)]),
     "attn_kv4_read": (READ, [dict(d=32), dict(page=1 << 20, n_pages=1 << 12),
-                             dict(B=1 << 16, N=1 << 16), dict(width=1 << 28)]),
+                             dict(B=1 << 16, N=1 << 16), dict(width=1 << 28),
+                             dict(N=1 << 29, Hkv=64, n_pages=1)]),
     "attn_kv4_fwd": (KV4, [dict(d=256), dict(page=1 << 20, n_pages=1 << 12), dict(width=1 << 28),
                            dict(B=1 << 20, Hq=1 << 12), dict(Nq=1 << 30),
                            dict(B=1 << 16, page=1 << 20, n_pages=1, width=1 << 10)]),
