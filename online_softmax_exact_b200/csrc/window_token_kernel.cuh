@@ -16,8 +16,8 @@
 // Half of a block's registers are always in flight: the next block's keys are fetched once
 // this one's scores are formed, its values once this one's products are issued.
 //
-// Measured: 4 requests, 32 query heads on 8, d = 128, window 4096: 14.5 us (67 MB, 4.6 TB/s)
-// and 3 us for the join; on 128-row tiles the same call took 65 us.
+// Measured: 4 requests, 32 query heads on 8, d = 128, window 4096: 14.5 us (67 MB, 4.6 TB/s),
+// 17.0 us with the join; on 128-row tiles the same call took 65 us.
 //
 // A weight P enters as the sum of two bf16 numbers (16 bits of it), the high part in the
 // even and the low part in the odd column of a query row: with four query rows to an
