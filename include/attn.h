@@ -374,7 +374,9 @@ attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32
  * request b has position p = q_pos[b] + i (q_pos NULL: lens[b] - Nq + i) and sees the
  * cached tokens j < lens[b] with j <= p and, when window > 0, (j > p - window or
  * j < sinks). Returns O and LSE as the other attention calls do (attn_merge joins them
- * with partials over other keys); rows that see no key give O = 0, LSE = -inf.
+ * with partials over other keys); rows that see no key give O = 0, LSE = -inf. What a token
+ * that a row does not see holds in the cache, or whether it was ever written, does not
+ * reach that row.
  *
  *   q        device, bf16 [B][Hq][Nq][d], 16-byte aligned
  *   table    device, int32 [B][width]; tokens on a page outside the cache are not seen

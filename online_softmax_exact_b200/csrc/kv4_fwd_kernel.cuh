@@ -601,15 +601,6 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
               par[r][0] = q.x, par[r][1] = q.y;
             }
           }
-          if constexpr (kEdge) {
-            // rows past the request's length may hold any bits: 0 * NaN is not 0
-            const int k0 = cur.s.block((st << p.stage_shift) + j) * 16;
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              if (k0 + 8 * r + g >= cur.s.len)
-#pragma unroll
-                for (int i = 0; i < kG; ++i) par[r][i] = 0u;
-          }
           uint32_t bp[NT][kG][2];
 #pragma unroll
           for (int i = 0; i < kG; ++i) {
@@ -617,12 +608,14 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                const float x = pr[nt][r] * param_scale(par[r][i]);
+                // a token that the row does not see may hold any bits: 0 * NaN is not 0
+                const uint32_t pm = kEdge && sc[j][nt][r] == -INFINITY ? 0u : par[r][i];
+                const float x = pr[nt][r] * param_scale(pm);
                 const float high = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
                 // (the low part is rounded, not cut: cut ones would all err to one side, and
                 // over a long context the small sums that are left show it)
                 bp[nt][i][r] = transpose_b16(pack_bf16x2(high, x - high));
-                zo[nt][i] = fmaf(pr[nt][r], param_zero(par[r][i]), zo[nt][i]);
+                zo[nt][i] = fmaf(pr[nt][r], param_zero(pm), zo[nt][i]);
               }
             }
           }

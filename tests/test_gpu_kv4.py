@@ -137,7 +137,7 @@ def test_read_past_the_table(osx):
 # --------------------------------------------------------------------------------- forward
 def fwd_case(osx, seed, B, Hq, Hkv, Nq, d, page, lens, window=0, sinks=0, q_pos=None, scale=None,
              o_dtype=torch.float32, qsize=1.0, max_len=0, bad_pages=(), width=None, table=None,
-             ksize=1.0, vsize=1.0):
+             ksize=1.0, vsize=1.0, poison_unseen=None):
     rng = np.random.default_rng(seed)
     lens = np.asarray(lens)
     if width is None:
@@ -159,6 +159,16 @@ def fwd_case(osx, seed, B, Hq, Hkv, Nq, d, page, lens, window=0, sinks=0, q_pos=
             row = p % 16
             for p0 in (4 * d, 4 * d + d // 2):
                 words[pg, :, p // 16, p0 + row * (d // 32):p0 + (row + 1) * (d // 32)] = 0x7fc07f80
+    if poison_unseen is not None:
+        # parameters of every token that no row of its request sees
+        for b in range(B):
+            n = int(min(max(lens[b], 0), width * page))
+            pos = (n - Nq if q_pos is None else q_pos[b]) + np.arange(Nq)
+            for p in np.flatnonzero(~su.visible(pos, np.arange(n), window, sinks).any(0)):
+                row = p % 16
+                for p0 in (4 * d, 4 * d + d // 2):
+                    words[table[b, p // page], :, p % page // 16,
+                          p0 + row * (d // 32):p0 + (row + 1) * (d // 32)] = poison_unseen
     words[sorted(set(range(n_pages)) - set(table.flat))] = 0xffffffff
     g = torch.Generator().manual_seed(seed)
     q = (torch.randn((B, Hq, Nq, d), generator=g) * qsize).to(torch.bfloat16)
@@ -236,6 +246,42 @@ def test_fwd_positions_of_the_callers_choice(osx, d):
     fwd_case(osx, 1, 6, 4, 2, 4, d, 16, lens, q_pos=pos)
     fwd_case(osx, 2, 6, 4, 2, 4, d, 16, lens, q_pos=pos, window=30, sinks=0)
     fwd_case(osx, 3, 6, 4, 2, 4, d, 16, lens, q_pos=pos, window=30, sinks=5)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bits", [0x7fc07fc0, 0x7f803f80, 0x3f807f80, 0xff80ff80])
+def test_fwd_unseen_tokens_hold_any_bits(osx, d, bits):
+    """Tokens before the window, between sinks and window, and behind the rows' positions
+    (never written, or another request's by now) share blocks with tokens that are seen:
+    NaN and infinities in their parameters do not reach the result."""
+    kw = dict(poison_unseen=bits)
+    fwd_case(osx, 21, 3, 4, 2, 1, d, 16, [600, 37, 303], window=70, **kw)
+    fwd_case(osx, 22, 3, 4, 2, 1, d, 16, [600, 37, 303], window=33, sinks=5, **kw)
+    fwd_case(osx, 23, 2, 8, 2, 5, d, 32, [600, 301], window=40, sinks=17, **kw)
+    fwd_case(osx, 24, 3, 4, 2, 3, d, 16, [200, 200, 200], q_pos=[0, 50, 120], **kw)
+    fwd_case(osx, 25, 2, 4, 4, 1, d, 64, [5000, 4000], window=2001, q_pos=[3000, 3999], **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq,Hq,n", [(3, 2, 100), (5, 4, 700), (8, 2, 33)])
+def test_fwd_token_seen_by_the_last_row_only(osx, d, Nq, Hq, n):
+    """NaN parameters of the newest token change no bit of the rows before it."""
+    rng = np.random.default_rng(n)
+    cache, _, _ = su.random_cache(rng, n // 16 + 1, 1, 16, d)
+    g = torch.Generator().manual_seed(n)
+    q = torch.randn((1, Hq, Nq, d), generator=g).to(torch.bfloat16).cuda()
+    table = i32(rng.permutation(n // 16 + 1)[None])
+
+    def run():
+        return osx.attn_kv4_fwd(q, torch.from_numpy(cache).cuda(), table, i32([n]))
+
+    o, lse = run()
+    words, row = cache.view(np.uint32), (n - 1) % 16
+    for p0 in (4 * d, 4 * d + d // 2):
+        words[int(table[0, (n - 1) // 16]), :, 0,
+              p0 + row * (d // 32):p0 + (row + 1) * (d // 32)] = 0x7fc07fc0
+    o2, lse2 = run()
+    assert torch.equal(o[:, :, :-1], o2[:, :, :-1]) and torch.equal(lse[:, :, :-1], lse2[:, :, :-1])
 
 
 @pytest.mark.parametrize("d", [64, 128])
