@@ -73,10 +73,6 @@ void* address(PyObject* o, ScalarType type, at::IntArrayRef shape, c10::Device d
   return address(cuda_tensor(o, name), type, shape, dev, name);
 }
 
-at::Tensor fresh(at::IntArrayRef shape, ScalarType type, c10::Device dev) {
-  return at::detail::empty_cuda(shape, type, dev, std::nullopt);
-}
-
 // A piece of a buffer as a tensor of its own: several small outputs of one allocation (an
 // allocation costs more than all the rest of a small call's marshalling).
 at::Tensor piece(const at::Tensor& buf, int64_t* at, at::IntArrayRef shape) {
@@ -87,15 +83,6 @@ at::Tensor piece(const at::Tensor& buf, int64_t* at, at::IntArrayRef shape) {
   impl->set_storage_offset(*at);
   impl->set_sizes_contiguous(shape);
   *at += c10::multiply_integers(shape);
-  return t;
-}
-
-// The given output, checked, or a new one.
-at::Tensor output(PyObject* o, at::IntArrayRef shape, ScalarType type, c10::Device dev,
-                  const char* name) {
-  if (o == Py_None) return fresh(shape, type, dev);
-  const at::Tensor& t = cuda_tensor(o, name);
-  address(t, type, shape, dev, name);
   return t;
 }
 
@@ -122,11 +109,49 @@ int size32(int64_t v, const char* name) {
   return static_cast<int>(v);
 }
 
-// A stream's handle: the given one (an integer), or the device's current stream.
-void* stream_of(PyObject* o, c10::Device dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-  return reinterpret_cast<void*>(integer(o));
-}
+// Where a call runs: its device, and the given stream (a handle, an integer) or the device's
+// current one. While it lives that stream is the current one, so what the call allocates comes
+// from its pool: a block that was freed on the caller's stream may still be in use there.
+class Launch {
+ public:
+  Launch(PyObject* o, c10::Device dev)
+      : dev_(dev), caller_(c10::cuda::getCurrentCUDAStream(dev.index())), guard_(pick(o)) {}
+
+  void* stream() const { return guard_.current_stream().stream(); }
+
+  // Memory for this call alone.
+  at::Tensor scratch(int64_t bytes) const { return empty({bytes}, ScalarType::Byte); }
+
+  // An output: the caller's stream is likely to use it next, and to be where it is dropped.
+  at::Tensor fresh(at::IntArrayRef shape, ScalarType type) const {
+    at::Tensor t = empty(shape, type);
+    if (guard_.current_stream() != caller_) t.record_stream(caller_);
+    return t;
+  }
+
+  // The given output, checked, or a new one.
+  at::Tensor output(PyObject* o, at::IntArrayRef shape, ScalarType type, const char* name) const {
+    if (o == Py_None) return fresh(shape, type);
+    const at::Tensor& t = cuda_tensor(o, name);
+    address(t, type, shape, dev_, name);
+    return t;
+  }
+
+ private:
+  at::Tensor empty(at::IntArrayRef shape, ScalarType type) const {
+    return at::detail::empty_cuda(shape, type, dev_, std::nullopt);
+  }
+  c10::cuda::CUDAStream pick(PyObject* o) const {
+    if (o == Py_None) return caller_;
+    auto s = reinterpret_cast<cudaStream_t>(integer(o));
+    if (s == cudaStreamLegacy) s = nullptr;  // the default stream has both names
+    return c10::cuda::getStreamFromExternal(s, dev_.index());
+  }
+
+  c10::Device dev_;
+  c10::cuda::CUDAStream caller_;
+  c10::cuda::CUDAStreamGuard guard_;
+};
 
 void check(attn_status_t st, const char* where) {
   if (st == ATTN_OK) return;
@@ -197,8 +222,8 @@ OSX_ENTRY(kv_plan, 8)
   const auto* free_p = static_cast<int32_t*>(
       address(free_pages, ScalarType::Int, free_pages.sizes(), dev, "free_pages"));
   const auto* head_p = static_cast<int32_t*>(address(a[4], ScalarType::Int, {1}, dev, "free_head"));
-  const c10::cuda::OptionalCUDAGuard guard(dev);
-  const at::Tensor buf = fresh({2 * B * n_new + 2 * B + 1}, ScalarType::Int, dev);
+  const Launch run(a[7], dev);
+  const at::Tensor buf = run.fresh({2 * B * n_new + 2 * B + 1}, ScalarType::Int);
   int64_t at = 0;
   at::Tensor slots = piece(buf, &at, {B, n_new}), pos = piece(buf, &at, {B, n_new});
   at::Tensor out = piece(buf, &at, {B}), served = piece(buf, &at, {B}), head = piece(buf, &at, {1});
@@ -208,7 +233,7 @@ OSX_ENTRY(kv_plan, 8)
                      static_cast<int32_t*>(out.data_ptr()), static_cast<int32_t*>(head.data_ptr()),
                      static_cast<int32_t*>(served.data_ptr()), size32(B, "B"), n_new,
                      size32(table.size(1), "width"), page, size32(free_pages.size(0), "free_pages"),
-                     stream_of(a[7], dev)),
+                     run.stream()),
         "attn_kv_plan");
   return pack(slots, pos, out, head, served);
 OSX_END
@@ -236,17 +261,17 @@ OSX_ENTRY(qk_norm_rope, 13)
   const auto* p_p = static_cast<int32_t*>(address(a[4], ScalarType::Int, {B, N}, dev, "positions"));
   const int inter = PyObject_IsTrue(a[8]);
   if (inter < 0) throw python_error();
-  const c10::cuda::OptionalCUDAGuard guard(dev);
-  at::Tensor q = output(a[9], {B, Hq, N, d}, ScalarType::BFloat16, dev, "q");
-  at::Tensor k = output(a[10], {B, Hkv, N, d}, ScalarType::BFloat16, dev, "k");
-  at::Tensor v = output(a[11], {B, Hkv, N, d}, ScalarType::BFloat16, dev, "v");
+  const Launch run(a[12], dev);
+  at::Tensor q = run.output(a[9], {B, Hq, N, d}, ScalarType::BFloat16, "q");
+  at::Tensor k = run.output(a[10], {B, Hkv, N, d}, ScalarType::BFloat16, "k");
+  at::Tensor v = run.output(a[11], {B, Hkv, N, d}, ScalarType::BFloat16, "v");
   // the stride of a dimension of one row is never used
   check(attn_qk_norm_rope(qkv.data_ptr(), B > 1 ? qkv.stride(0) : 0, N > 1 ? qkv.stride(1) : 0, wq_p,
                           wk_p, wq.scalar_type() == ScalarType::Float, f_p,
                           static_cast<int>(inv.size(0)), p_p, q.data_ptr(), k.data_ptr(),
                           v.data_ptr(), size32(B, "B"), size32(N, "N"), Hq, Hkv,
                           static_cast<int>(d), static_cast<float>(real(a[7])), inter,
-                          stream_of(a[12], dev)),
+                          run.stream()),
         "attn_qk_norm_rope");
   return pack(q, k, v);
 OSX_END
@@ -263,9 +288,9 @@ OSX_ENTRY(kv4_append, 5)
   const void* k_p = address(k, ScalarType::BFloat16, k.sizes(), dev, "k");
   const void* v_p = address(a[1], ScalarType::BFloat16, k.sizes(), dev, "v");
   const auto* s_p = static_cast<int32_t*>(address(a[3], ScalarType::Int, {B, N}, dev, "slots"));
-  const c10::cuda::OptionalCUDAGuard guard(dev);
+  const Launch run(a[4], dev);
   check(attn_kv4_append(k_p, v_p, c.p, s_p, size32(B, "B"), c.Hkv, size32(N, "N"), c.d, c.page,
-                        c.n_pages, stream_of(a[4], dev)),
+                        c.n_pages, run.stream()),
         "attn_kv4_append");
   Py_RETURN_NONE;
 OSX_END
@@ -281,11 +306,11 @@ OSX_ENTRY(kv4_read, 8)
   const auto* t_p = static_cast<int32_t*>(address(table, ScalarType::Int, table.sizes(), dev, "table"));
   const auto* s_p = static_cast<int32_t*>(address(a[2], ScalarType::Int, {B}, dev, "start"));
   const auto* l_p = static_cast<int32_t*>(address(a[3], ScalarType::Int, {B}, dev, "lens"));
-  const c10::cuda::OptionalCUDAGuard guard(dev);
-  at::Tensor k = output(a[5], {B, c.Hkv, n_tok, c.d}, ScalarType::BFloat16, dev, "k");
-  at::Tensor v = output(a[6], {B, c.Hkv, n_tok, c.d}, ScalarType::BFloat16, dev, "v");
+  const Launch run(a[7], dev);
+  at::Tensor k = run.output(a[5], {B, c.Hkv, n_tok, c.d}, ScalarType::BFloat16, "k");
+  at::Tensor v = run.output(a[6], {B, c.Hkv, n_tok, c.d}, ScalarType::BFloat16, "v");
   check(attn_kv4_read(c.p, t_p, s_p, l_p, k.data_ptr(), v.data_ptr(), size32(B, "B"), c.Hkv, n_tok,
-                      c.d, c.page, c.n_pages, size32(table.size(1), "width"), stream_of(a[7], dev)),
+                      c.d, c.page, c.n_pages, size32(table.size(1), "width"), run.stream()),
         "attn_kv4_read");
   return pack(k, v);
 OSX_END
@@ -319,19 +344,17 @@ OSX_ENTRY(kv4_fwd, 13)
                         ? nullptr
                         : static_cast<int32_t*>(address(a[4], ScalarType::Int, {B}, dev, "q_pos"));
   const ScalarType type = o_type(a[10], a[9]);
-  const c10::cuda::OptionalCUDAGuard guard(dev);
-  at::Tensor o = output(a[10], {B, Hq, Nq, d}, type, dev, "o");
-  at::Tensor lse = output(a[11], {B, Hq, Nq}, ScalarType::Float, dev, "lse");
+  const Launch run(a[12], dev);
+  at::Tensor o = run.output(a[10], {B, Hq, Nq, d}, type, "o");
+  at::Tensor lse = run.output(a[11], {B, Hq, Nq}, ScalarType::Float, "lse");
   const int b = size32(B, "B"), hq = size32(Hq, "Hq"), nq = size32(Nq, "Nq");
   const int64_t n_ws = attn_kv4_fwd_workspace(b, hq, c.Hkv, nq, c.d);
-  void* s = stream_of(a[12], dev);
-  at::Tensor ws = fresh({n_ws}, ScalarType::Byte, dev);
-  if (a[12] != Py_None)  // freed on this function's return, used on the other stream
-    ws.record_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), dev.index()));
+  at::Tensor ws = run.scratch(n_ws);
   check(attn_kv4_fwd(q_p, c.p, t_p, l_p, p_p, o.data_ptr(), static_cast<float*>(lse.data_ptr()),
                      type == ScalarType::BFloat16, b, hq, c.Hkv, nq, c.d, c.page, c.n_pages,
                      size32(table.size(1), "width"), integer(a[8]), integer32(a[5], "window"),
-                     integer32(a[6], "sinks"), static_cast<float>(real(a[7])), ws.data_ptr(), n_ws, s),
+                     integer32(a[6], "sinks"), static_cast<float>(real(a[7])), ws.data_ptr(), n_ws,
+                     run.stream()),
         "attn_kv4_fwd");
   return pack(o, lse);
 OSX_END
@@ -360,22 +383,18 @@ OSX_ENTRY(window_fwd, 13)
   const void* k_p = address(k, ScalarType::BFloat16, k.sizes(), dev, "k");
   const void* v_p = address(a[2], ScalarType::BFloat16, k.sizes(), dev, "v");
   const ScalarType type = o_type(a[10], a[9]);
-  const c10::cuda::OptionalCUDAGuard guard(dev);
-  at::Tensor o = output(a[10], {B, Hq, Nq, d}, type, dev, "o");
-  at::Tensor lse = output(a[11], {B, Hq, Nq}, ScalarType::Float, dev, "lse");
+  const Launch run(a[12], dev);
+  at::Tensor o = run.output(a[10], {B, Hq, Nq, d}, type, "o");
+  at::Tensor lse = run.output(a[11], {B, Hq, Nq}, ScalarType::Float, "lse");
   const int b = size32(B, "B"), hq = size32(Hq, "Hq"), hkv = size32(Hkv, "Hkv");
   const int64_t n_ws = attn_window_fwd_workspace(b, hq, hkv, Nq, static_cast<int>(d));
-  void* s = stream_of(a[12], dev);
   at::Tensor ws;
-  if (n_ws > 0) {
-    ws = fresh({n_ws}, ScalarType::Byte, dev);
-    if (a[12] != Py_None)  // freed on this function's return, used on the other stream
-      ws.record_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), dev.index()));
-  }
+  if (n_ws > 0) ws = run.scratch(n_ws);
   check(attn_window_fwd(q_p, k_p, v_p, o.data_ptr(), static_cast<float*>(lse.data_ptr()),
                         type == ScalarType::BFloat16, b, hq, hkv, Nq, n_keys, Nq, L, q_off, kv_off,
                         size32(d, "d"), integer32(a[3], "window"), integer32(a[4], "sinks"),
-                        static_cast<float>(real(a[8])), n_ws > 0 ? ws.data_ptr() : nullptr, n_ws, s),
+                        static_cast<float>(real(a[8])), n_ws > 0 ? ws.data_ptr() : nullptr, n_ws,
+                        run.stream()),
         "attn_window_fwd");
   return pack(o, lse);
 OSX_END

@@ -26,22 +26,18 @@ __all__ = ["kv4_cache", "attn_kv_plan", "attn_qk_norm_rope", "attn_kv4_append", 
 
 
 def _handle(stream, tensors):
-    """The handle of a given stream (an integer is one already). Tensors used on a stream
-    other than the one they were made on are recorded there, so that their memory is not
-    reused too early."""
+    """The handle of a given stream (an integer is one already, None the current stream).
+    Given tensors are recorded on a stream object, so that their memory is not reused too
+    early; with an integer they have to live until the stream is done with them. What a
+    call allocates comes from its stream's memory, recorded on the caller's stream."""
+    if stream is None:
+        return None
     if not hasattr(stream, "cuda_stream"):
         return int(stream)
     for t in tensors:
         if isinstance(t, torch.Tensor) and t.is_cuda:
             t.record_stream(stream)
     return int(stream.cuda_stream)
-
-
-def _outputs_too(stream, out):
-    if hasattr(stream, "cuda_stream"):
-        for t in out:
-            t.record_stream(stream)
-    return out
 
 
 def kv4_cache(n_pages: int, n_kv_heads: int, d: int, *, page_size: int = 64,
@@ -62,11 +58,8 @@ def attn_kv_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor
     free_pages int32 [F], taken from free_head (int32 [1]) on. Returns (slots [B, n_new],
     positions [B, n_new], lens [B], free_head [1], served [B]), all int32: slots are -1
     behind a request's tokens and where it was not served (served 0, length unchanged)."""
-    if stream is None:
-        return _native().kv_plan(lens, new_lens, table, free_pages, free_head, page_size, n_new, None)
     h = _handle(stream, (lens, new_lens, table, free_pages, free_head))
-    return _outputs_too(stream, _native().kv_plan(lens, new_lens, table, free_pages, free_head,
-                                                  page_size, n_new, h))
+    return _native().kv_plan(lens, new_lens, table, free_pages, free_head, page_size, n_new, h)
 
 
 def attn_qk_norm_rope(qkv: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor,
@@ -78,20 +71,16 @@ def attn_qk_norm_rope(qkv: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor,
     qkv bf16 [B, N, (n_heads + 2 n_kv_heads) d] (its rows may be strided); wq, wk [d] bf16
     or fp32; inv_freq fp32 [r / 2] for the first r values of a head (r / 2 a multiple of 8);
     positions int32 [B, N]. Returns bf16 (q [B, n_heads, N, d], k, v [B, n_kv_heads, N, d])."""
-    if stream is None:
-        return _native().qk_norm_rope(qkv, wq, wk, inv_freq, positions, n_heads, n_kv_heads, eps,
-                                      interleaved, q, k, v, None)
-    h = _handle(stream, (qkv, wq, wk, inv_freq, positions))
-    return _outputs_too(stream, _native().qk_norm_rope(qkv, wq, wk, inv_freq, positions, n_heads,
-                                                       n_kv_heads, eps, interleaved, q, k, v, h))
+    h = _handle(stream, (qkv, wq, wk, inv_freq, positions, q, k, v))
+    return _native().qk_norm_rope(qkv, wq, wk, inv_freq, positions, n_heads, n_kv_heads, eps,
+                                  interleaved, q, k, v, h)
 
 
 def attn_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor, *,
                     stream=None) -> None:
     """Tokens into the 4-bit cache: k, v bf16 [B, Hkv, N, d], slots int32 [B, N] (distinct;
     a negative slot, or one outside the cache, skips its token)."""
-    h = None if stream is None else _handle(stream, (k, v, cache, slots))
-    _native().kv4_append(k, v, cache, slots, h)
+    _native().kv4_append(k, v, cache, slots, _handle(stream, (k, v, cache, slots)))
 
 
 def attn_kv4_read(cache: torch.Tensor, table: torch.Tensor, start: torch.Tensor,
@@ -99,10 +88,8 @@ def attn_kv4_read(cache: torch.Tensor, table: torch.Tensor, start: torch.Tensor,
                   v: torch.Tensor | None = None, stream=None):
     """Tokens [start[b], start[b] + n) of each request out of the 4-bit cache, as bf16
     (k, v [B, Hkv, n, d]); zeros at and past lens[b]. start, lens int32 [B]."""
-    if stream is None:
-        return _native().kv4_read(cache, table, start, lens, n, k, v, None)
-    h = _handle(stream, (cache, table, start, lens))
-    return _outputs_too(stream, _native().kv4_read(cache, table, start, lens, n, k, v, h))
+    h = _handle(stream, (cache, table, start, lens, k, v))
+    return _native().kv4_read(cache, table, start, lens, n, k, v, h)
 
 
 def _is_bf16(o_dtype) -> bool:
@@ -127,12 +114,9 @@ def attn_kv4_fwd(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens
     bf16 = _is_bf16(o_dtype)
     if scale is None:
         scale = 1.0 if not isinstance(q, torch.Tensor) or q.dim() != 4 else q.shape[3] ** -0.5
-    if stream is None:
-        return _native().kv4_fwd(q, cache, table, lens, q_pos, window, sinks, scale, max_len, bf16, o,
-                                 lse, None)
-    h = _handle(stream, (q, cache, table, lens, q_pos))
-    return _outputs_too(stream, _native().kv4_fwd(q, cache, table, lens, q_pos, window, sinks, scale,
-                                                  max_len, bf16, o, lse, h))
+    h = _handle(stream, (q, cache, table, lens, q_pos, o, lse))
+    return _native().kv4_fwd(q, cache, table, lens, q_pos, window, sinks, scale, max_len, bf16, o, lse,
+                             h)
 
 
 def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, window: int,
@@ -148,9 +132,5 @@ def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, window
     bf16 = _is_bf16(o_dtype)
     if scale is None:
         scale = 1.0 if not isinstance(q, torch.Tensor) or q.dim() != 4 else q.shape[3] ** -0.5
-    if stream is None:
-        return _native().window_fwd(q, k, v, window, sinks, q_off, kv_off, kv_len, scale, bf16, o, lse,
-                                    None)
-    h = _handle(stream, (q, k, v))
-    return _outputs_too(stream, _native().window_fwd(q, k, v, window, sinks, q_off, kv_off, kv_len,
-                                                     scale, bf16, o, lse, h))
+    h = _handle(stream, (q, k, v, o, lse))
+    return _native().window_fwd(q, k, v, window, sinks, q_off, kv_off, kv_len, scale, bf16, o, lse, h)
