@@ -47,7 +47,10 @@
 // again: 570 warp instructions per block of 16 tokens, and as subnormals 330.
 //
 // Pages are looked up in the table and checked against n_pages: keys on a page outside
-// the cache are invisible. Rows of a page past a request's length may hold anything.
+// the cache are invisible. Rows of a page past a request's length may hold anything. Lengths,
+// positions and the table are plain loads: the launch before this one (the plan, say) may
+// write them while this kernel's blocks are already resident, which the read-only path
+// (ld.global.nc) does not allow for.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -105,11 +108,11 @@ struct Kv4Span {
 __device__ __forceinline__ Kv4Span kv4_span(const Kv4FwdParams& p, int b) {
   Kv4Span s;
   const long long room = (long long)p.width * p.blocks_per_page * 16;
-  int len = __ldg(p.lens + b);
+  int len = p.lens[b];
   if (len < 0) len = 0;
   if (len > room) len = (int)room;
   s.len = len;
-  s.p0 = p.q_pos ? (long long)__ldg(p.q_pos + b) : (long long)len - p.Nq;
+  s.p0 = p.q_pos ? (long long)p.q_pos[b] : (long long)len - p.Nq;
   const long long hi_l = s.p0 + p.Nq < len ? s.p0 + p.Nq : len;  // keys below may be seen
   const int hi = hi_l > 0 ? (int)hi_l : 0;
   const long long lo_l = p.window ? s.p0 - p.window + 1 : 0;
@@ -315,7 +318,7 @@ kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
       const int lb = fet.s.block(bi);
       const int pg = quotient(lb, p.blocks_per_page, p.page_magic);
       in_page = lb - pg * p.blocks_per_page;
-      page_next = __ldg(p.table + (long long)fet.b * p.width + pg);
+      page_next = p.table[(long long)fet.b * p.width + pg];
     }
   };
   int fetch_stage = fet.stage;
