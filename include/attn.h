@@ -382,7 +382,9 @@ attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32
  *   table    device, int32 [B][width]; tokens on a page outside the cache are not seen
  *   lens     device, int32 [B]; a negative length counts as 0, one beyond the table
  *            (width * page_size) as the table's end
- *   q_pos    device, int32 [B], or NULL
+ *   q_pos    device, int32 [B], or NULL. Needed where the requests of a call add different
+ *            numbers of tokens: their first new positions, the lengths before attn_kv_plan
+ *            (rows behind a request's new tokens are padding)
  *   o        device, [B][Hq][Nq][d], fp32 (o_bf16 = 0) or bf16 (o_bf16 = 1), 16-byte aligned
  *   lse      device, fp32 [B][Hq][Nq]
  *   max_len  the longest request's length as far as the caller knows (0: unknown, the

@@ -5,14 +5,16 @@ Thin bindings over the entry points of the same names in ``include/attn.h``: the
 torch tensors, allocate the outputs that are not given (and workspaces), and launch on the
 tensors' device and its current stream (or ``stream``). The marshalling is native
 (``csrc/serving_binding.cpp``): a decode step's kernels take microseconds, and so do calls.
-One decoder layer's step over a batch of requests reads::
+A whole prompt can run through ``attn_window_fwd(q, k, v, window=W, sinks=S)`` on the bf16
+tensors. One decoder layer's step over a batch of requests, of which request b adds
+new_lens[b] <= N tokens, the first at position lens[b]::
 
-    slots, pos, lens, head, served = attn_kv_plan(lens, new_lens, table, free, head,
-                                                  page_size=cache.shape[2] * 16, n_new=N)
+    slots, pos, grown, head, served = attn_kv_plan(lens, new_lens, table, free, head,
+                                                   page_size=cache.shape[2] * 16, n_new=N)
     q, k, v = attn_qk_norm_rope(qkv, wq, wk, inv_freq, pos, n_heads=Hq, n_kv_heads=Hkv)
     attn_kv4_append(k, v, cache, slots)
-    o, lse = attn_kv4_fwd(q, cache, table, lens)            # or, for a whole prompt,
-    o, lse = attn_window_fwd(q, k, v, window=W, sinks=S)    # on the bf16 tensors
+    o, lse = attn_kv4_fwd(q, cache, table, grown, q_pos=lens)
+    lens = grown
 """
 
 from __future__ import annotations
@@ -107,7 +109,8 @@ def attn_kv4_fwd(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens
                  lse: torch.Tensor | None = None, stream=None):
     """Attention of each request's newest tokens over the 4-bit cache. q bf16
     [B, Hq, Nq, d]; table int32 [B, width]; lens int32 [B], the tokens cached (the queries'
-    own among them). Query i has position lens[b] - Nq + i, or q_pos[b] + i (int32 [B]);
+    own among them). Query i has position lens[b] - Nq + i, or q_pos[b] + i (int32 [B]):
+    give q_pos where requests add different numbers of tokens (rows behind them are padding);
     with a window it sees the last ``window`` positions and the first ``sinks``.
     ``max_len``: the longest length, if the host knows it (a hint). Returns
     (O [B, Hq, Nq, d] of o_dtype, LSE fp32 [B, Hq, Nq])."""
