@@ -113,6 +113,16 @@ def load() -> ctypes.CDLL:
 _serving = None
 
 
+def binding_target() -> str:
+    """What the serving binding is compiled against: it uses torch's C++ interface, which
+    changes from version to version, and Python's."""
+    import sys
+
+    import torch
+
+    return f"torch {torch.__version__}, python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
 def load_serving():
     """The native binding of the serving operators (built by ``build.py``)."""
     global _serving
@@ -131,6 +141,9 @@ def load_serving():
         spec = importlib.util.spec_from_file_location("_serving", BINDING_PATH, loader=loader)
         mod = importlib.util.module_from_spec(spec)
         loader.exec_module(mod)
+        if mod.built_for != binding_target():
+            raise ImportError(f"{BINDING_PATH} was built for {mod.built_for}, this is"
+                              f" {binding_target()}: build it again")
         mod.set_error(AttnError)
         _serving = mod
     return _serving

@@ -11,6 +11,8 @@ import subprocess
 import sys
 from pathlib import Path
 
+from ._abi import binding_target
+
 PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 ROOT = PKG.parent
@@ -18,6 +20,7 @@ BUILD = ROOT / "_build"
 LIB = PKG / "libattn.so"
 BINDING = PKG / "_serving.so"  # the serving operators' torch binding, linked to libattn.so
 BINDING_SOURCE = "serving_binding.cpp"
+BINDING_STAMP = BUILD / "serving_binding.txt"  # what it was compiled against
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -47,12 +50,16 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     serving operators' torch binding beside it."""
     if force or _stale(LIB, SOURCES + DEPS):
         _build_lib(verbose)
-    if force or _stale(BINDING, [BINDING_SOURCE]):
-        _build_binding()
+    target = binding_target()
+    built_for = BINDING_STAMP.read_text() if BINDING_STAMP.exists() else None
+    if force or _stale(BINDING, [BINDING_SOURCE]) or built_for != target:
+        _build_binding(target)
+        BUILD.mkdir(exist_ok=True)
+        BINDING_STAMP.write_text(target)
     return LIB
 
 
-def _build_binding() -> None:
+def _build_binding(target: str) -> None:
     import sysconfig
 
     import torch
@@ -63,6 +70,7 @@ def _build_binding() -> None:
     tmp = BINDING.with_suffix(f".{os.getpid()}.tmp.so")
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unknown-pragmas",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DOSX_BUILT_FOR="{target}"',
            *[f"-isystem{p}" for p in include_paths(device_type="cuda")],
            f"-isystem{sysconfig.get_paths()['include']}", str(CSRC / BINDING_SOURCE), "-o", str(tmp),
            *[f"-L{p}" for p in libs], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch",

@@ -418,4 +418,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__serving(void) { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__serving(void) {
+  PyObject* m = PyModule_Create(&g_module);
+  // (the versions that the build compiled against; the loader compares them)
+  if (m && PyModule_AddStringConstant(m, "built_for", OSX_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}
