@@ -395,8 +395,8 @@ attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32
  *   workspace  device, 16-byte aligned, at least attn_kv4_fwd_workspace(...) bytes (about
  *            5 MB); its contents on entry do not matter, and nothing in it is kept. Calls
  *            whose work may overlap on the GPU need workspaces of their own.
- * Query rows may be of any size below 2^112. Cached values may be up to 2^24 in magnitude,
- * and the scales of the values' groups 2^-40 or more (a group of values with a smaller one
+ * Query rows, the scale, and their product may be of any size below 2^112 (the scale's factor
+ * leaves fp32 beyond). Cached values may be up to 2^24 in magnitude, and the scales of the values' groups 2^-40 or more (a group of values with a smaller one
  * counts as its zero point, about). The same inputs give the same bits.
  */
 attn_status_t attn_kv4_fwd(const void* q, const void* cache, const int32_t* table,
