@@ -51,9 +51,9 @@ unsigned grid_1d(long long blocks) {
   return blocks > 0 && blocks <= 0x7fffffffLL ? static_cast<unsigned>(blocks) : 0u;
 }
 
-// Function attributes of a kernel, set once per device.
+// A kernel's shared memory limit, set once per device.
 template <auto kKernel>
-int prepare_kernel(uint32_t smem, bool clusters) {
+int prepare_kernel(uint32_t smem) {
   constexpr int kMaxDevices = 64;
   static std::mutex mutex;
   static bool ready[kMaxDevices];
@@ -63,9 +63,6 @@ int prepare_kernel(uint32_t smem, bool clusters) {
   if (ready[dev]) return ATTN_OK;
   if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
-    return ATTN_ERR_CUDA;
-  if (clusters && cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                                       1) != cudaSuccess)
     return ATTN_ERR_CUDA;
   ready[dev] = true;
   return ATTN_OK;
@@ -110,7 +107,7 @@ int launch_kv4_fwd_dn(Kv4FwdParams p, long long max_len, int num_sms, cudaStream
   }
   static_assert(C::kSB == 2 || C::kSB == 4, "blocks of a stage");
   if (items * stages < grid) grid = (int)(items * stages);
-  const int rc = prepare_kernel<kv4_fwd_kernel<D, NT>>(C::kSmemBytes, false);
+  const int rc = prepare_kernel<kv4_fwd_kernel<D, NT>>(C::kSmemBytes);
   if (rc != ATTN_OK) return rc;
   const int st =
       launch_dependent(kv4_fwd_kernel<D, NT>, grid, C::kWarps * 32, C::kSmemBytes, stream, p);
@@ -225,7 +222,7 @@ int launch_window_d(const WindowLaunch& a, const DeviceProps& dp, cudaStream_t s
                                 : ((cut + per_block - 1) / per_block < p.row_blocks
                                        ? (cut + per_block - 1) / per_block
                                        : p.row_blocks));
-  const int rc = prepare_kernel<attn_window_kernel<D>>(C::kSmemBytes, false);
+  const int rc = prepare_kernel<attn_window_kernel<D>>(C::kSmemBytes);
   if (rc != ATTN_OK) return rc;
   const int grid = units < dp.num_sms ? (int)units : dp.num_sms;
   return launch_dependent(attn_window_kernel<D>, grid, C::kThreads, C::kSmemBytes, stream, tq, tk,
