@@ -282,8 +282,9 @@ attn_status_t attn_ring_fwd_host_noalloc(const void* q_h, const void* k_h, const
  *
  * The 4-bit cache. Keys and values of one token and key/value head are stored in groups of
  * 32 values: zero = min (+0 for -0), scale = bf16((max - min) / 15), code =
- * rint((x - zero) / scale) (ties to the even code; 0 where the scale is 0), value = code * scale + zero; 4 bits a code and a bf16 scale and
- * zero point a group, 5 bits a value. Inputs must be finite and at most 2^126 in
+ * rint((x - zero) / scale) (differences in fp32, quotients correctly rounded, ties to the
+ * even code; 0 where the scale is 0), value = code * scale + zero; 4 bits a code and a bf16
+ * scale and zero point a group, 5 bits a value. Inputs must be finite and at most 2^126 in
  * magnitude; a group with other values reads back as unspecified values, its neighbours
  * are not affected. The cache is one buffer of
  *     n_pages * Hkv * page_size / 16 * 20 * d  bytes, 16-byte aligned:
@@ -333,7 +334,8 @@ attn_status_t attn_kv_plan(const int32_t* lens, const int32_t* new_lens, int32_t
  * calls take. Per query or key head row x: y = x * rsqrt(mean(x^2) + eps) * w, then the
  * pairs (y[j], y[j + n_freq]) (interleaved = 0) or (y[2j], y[2j + 1]) (interleaved = 1),
  * j < n_freq, turn by the angle positions[b][i] * inv_freq[j]; values from 2 n_freq on
- * stay. Value heads are copied. fp32 throughout (angles in fp64), rounded to bf16 once.
+ * stay. Value heads are copied. fp32 throughout (angles in fp64), rounded to bf16 once;
+ * values of query and key rows below 2^60 in magnitude (their squares are summed in fp32).
  *
  *   qkv        device, bf16; row (b, i) at qkv + b * stride_b + i * stride_n (elements,
  *              multiples of 8) holds Hq query, Hkv key and Hkv value heads of d values;
@@ -362,7 +364,7 @@ attn_status_t attn_kv4_append(const void* k, const void* v, void* cache, const i
 /*
  * attn_kv4_read - tokens [start[b], start[b] + N) of each request out of the 4-bit cache,
  * as the bf16 tensors the attention calls take (k, v [B][Hkv][N][d], 16-byte aligned,
- * written; values rounded to bf16 once). Rows at or past lens[b], rows on a page outside
+ * written; values in fp32, then rounded to bf16). Rows at or past lens[b], rows on a page outside
  * the cache or the table, and all rows of a request with a negative start are zero.
  */
 attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32_t* start,
@@ -392,12 +394,20 @@ attn_status_t attn_kv4_read(const void* cache, const int32_t* table, const int32
  *            definition.
  *   window   0 (none) or the window's length; sinks >= 0 counts only with a window
  *   scale    finite, > 0
- *   workspace  device, 16-byte aligned, at least attn_kv4_fwd_workspace(...) bytes (about
- *            5 MB); its contents on entry do not matter, and nothing in it is kept. Calls
- *            whose work may overlap on the GPU need workspaces of their own.
+ *   workspace  device, 16-byte aligned, at least attn_kv4_fwd_workspace(...) bytes (some 1 to
+ *            6 MB, and 1 to 4 KB for each request, key/value head and tile of up to 8 rows,
+ *            a row being a head of the group at a position). Its contents on entry do not
+ *            matter, and nothing in it is kept. Calls whose work may overlap on the GPU need
+ *            workspaces of their own.
  * Query rows, the scale, and their product may be of any size below 2^112 (the scale's factor
- * leaves fp32 beyond). Cached values may be up to 2^24 in magnitude, and the scales of the values' groups 2^-40 or more (a group of values with a smaller one
- * counts as its zero point, about). The same inputs give the same bits.
+ * leaves fp32 beyond). Cached values may be up to 2^24 in magnitude, and the scales of the
+ * values' groups 2^-40 or more (a group of values with a smaller one counts as its zero
+ * point, about). The same inputs give the same bits.
+ * The cache is read and unpacked once for every 4 (up to 4 rows a key/value head) or 8 rows, so
+ * a long chunk over a cached history is better served by attn_kv4_read and a bf16 call,
+ * merged with the chunk's own: over 32 768 tokens of one request, 32 heads on 8, d = 128, 64
+ * query tokens take 414 us here and 513 us by attn_kv4_read and attn_fwd_partial, 128 tokens
+ * 805 and 514 us, one token 29 and 513 us.
  */
 attn_status_t attn_kv4_fwd(const void* q, const void* cache, const int32_t* table,
                            const int32_t* lens, const int32_t* q_pos, void* o, float* lse,
@@ -420,7 +430,8 @@ int64_t attn_kv4_fwd_workspace(int B, int Hq, int Hkv, int Nq, int d);
  *
  *   q        device, bf16 parent [B][Hq][q_ld][d], rows [0, Nq) of it
  *   k, v     device, bf16 parents [B][Hkv][kv_ld][d], rows [0, Nkv): rows beyond are never
- *            read; rows within must be finite
+ *            read; rows within must be finite, also where no query row sees them (unlike
+ *            attn_kv4_fwd's tokens: a row not seen enters products with weight 0)
  *   o        device, dense [B][Hq][Nq][d], fp32 (o_bf16 = 0) or bf16 (o_bf16 = 1)
  *   lse      device, fp32 [B][Hq][Nq]
  *   window >= 1, sinks >= 0; scale finite, > 0; d in {64, 128}
@@ -428,6 +439,9 @@ int64_t attn_kv4_fwd_workspace(int B, int Hq, int Hkv, int Nq, int d);
  *            call of few query rows splits its keys and joins the parts there. May be NULL
  *            where that is 0. Its contents on entry do not matter, and nothing in it is
  *            kept; calls whose work may overlap on the GPU need workspaces of their own.
+ * Sums and softmax statistics are fp32. The weights of V's rows are bf16 numbers: one each
+ * (2^-8 of a weight) on 128-row tiles, as in attn_fwd, and the sum of two (2^-15 of it)
+ * where few query rows take the form that needs a workspace.
  */
 attn_status_t attn_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
                               int o_bf16, int B, int Hq, int Hkv, int64_t Nq, int64_t Nkv,

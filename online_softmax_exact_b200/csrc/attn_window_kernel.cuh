@@ -17,6 +17,9 @@
 //   * tiles cut by a row's limits (about two of nine) mask element by element, from one
 //     bit mask per row and 32 keys; the scores are then reduced by the same code as in
 //     whole tiles, a masked score being -inf.
+// P enters P.V as one bf16 number, rounded, as in attn_fwd_kernel (32k rows, bf16 output:
+// error against 64 bits 0.0023, of which the output's own rounding is 0.0016). A second part,
+// as in window_token_kernel.cuh, would double the P.V product.
 // Bound: as in attn_fwd_kernel the tensor core and the exponentials of the visited tiles.
 // Measured: 32 768 rows, 32 heads on 8, window 1024, 64 sinks: 657 us in a short run (1.05
 // PFLOP/s of visited tiles), 753 us under the power cap; pairs of row tiles of one head took

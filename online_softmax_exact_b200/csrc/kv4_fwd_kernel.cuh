@@ -41,10 +41,11 @@
 //     results do not depend on timing). A unit that lies within one warp's run is finished
 //     there. Warp w's partial of unit u has slot w + u: both only grow along the stages.
 // Statistics and sums are fp32.
-// Measured (32 query heads on 8, d = 128): 131 072 tokens 40 us (168 MB, 4.2 TB/s with start
-// and join; the fetches alone, with start and join, 33 us); 32 requests of up to 8 192
-// tokens 54 us (224 MB; fetches alone 46 us). Codes as 128 + c with the bias taken out
-// again: 570 warp instructions per block of 16 tokens, and as subnormals 330.
+// Measured (32 query heads on 8, d = 128): 131 072 tokens 40 us (168 MB; the attention launch
+// by itself 39 us, 4.4 TB/s); 32 requests of up to 8 192 tokens 53 to 57 us (224 MB; by itself 51
+// us). 270 warp instructions a block of 16 tokens and head; instructions issue in 46% of the
+// cycles and the ALU pipe is busy in 47%: what bounds it is latency, since a warp fetches
+// into a slot only once it has computed on it.
 //
 // Pages are looked up in the table and checked against n_pages: keys on a page outside
 // the cache are invisible. Rows of a page past a request's length may hold anything. Lengths,
@@ -67,10 +68,10 @@ namespace osx {
 
 template <int D, int NT>
 struct Kv4FwdCfg {
-    // Eight warps of 255 registers, so that a stage's blocks run interleaved. Measured at
+  // Eight warps of 255 registers, so that a stage's blocks run interleaved. Measured at
   // NT = 1, d = 128 (128k tokens / ragged batch of 32, us): 8 warps, stages of 4 blocks 40.7
   // / 56.0; 16 warps, stages of 2 (a block at a time in registers) 42.8 / 57.2; 12 warps,
-  // stages of 3 42.0 / 56.5; the same ring without any compute 33.1 / 45.9.
+  // stages of 3 42.0 / 56.5.
   static constexpr int kWarps = 8;
   static constexpr int kRows = 4 * NT;
   static constexpr int kSB = D == 128 && NT == 2 ? 2 : 4;  // blocks of 16 tokens per stage

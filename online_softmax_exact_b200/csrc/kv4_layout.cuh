@@ -5,8 +5,9 @@
 //   zero = min, scale = bf16((max - min) / 15), code = rint((x - zero) / scale) in 0..15,
 //   value = code * scale + zero,
 // 5 bits a value in all. The inputs are bf16, so the zero point is exact; the scale is
-// rounded to the nearest bf16 (a 2^-9 relative change of the step, and the codes are
+// rounded to the nearest bf16 (a relative change of the step by up to 2^-8, and the codes are
 // taken against the rounded scale, so no value moves by more than half a step plus that).
+// Differences are taken in fp32.
 //
 // Pages hold page_size tokens (a multiple of 16) of every key/value head:
 //   cache[page][kv head][block], block = 16 tokens = 20 d bytes (2560 at d = 128):
@@ -65,7 +66,8 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t w, int e) {
 
 // Division by multiplication and fma: with r = RN(1/b), q = RN(a r) and e = a - q b (exact
 // by fma), RN(q + e r) is RN(a / b) away from under- and overflow (Markstein's theorem, for
-// b whose significand is not all ones; here 15, and scales of 8 significant bits).
+// b whose significand is not all ones; here 15, and scales of 8 significant bits, for all of
+// which one Newton step from an approximation within 2 units in the last place gives RN(1/b)).
 __device__ __forceinline__ float divide_fma(float a, float b, float r) {
   const float q = a * r;
   return fmaf(fmaf(-q, b, a), r, q);

@@ -59,7 +59,8 @@ def attn_kv_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor
     tokens. lens, new_lens int32 [B]; table int32 [B, width], new pages entered in place;
     free_pages int32 [F], taken from free_head (int32 [1]) on. Returns (slots [B, n_new],
     positions [B, n_new], lens [B], free_head [1], served [B]), all int32: slots are -1
-    behind a request's tokens and where it was not served (served 0, length unchanged)."""
+    behind a request's tokens and where it was not served (served 0, length unchanged). The
+    five share one allocation: clone what outlives the step by long, or is to be saved."""
     h = _handle(stream, (lens, new_lens, table, free_pages, free_head))
     return _native().kv_plan(lens, new_lens, table, free_pages, free_head, page_size, n_new, h)
 
@@ -131,7 +132,8 @@ def attn_window_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, window
     [B, Hkv, L, d], of which the first kv_len rows (default all) hold keys. Row i has
     position q_off + i, key j kv_off + j; q_off defaults to kv_off + kv_len - Nq (the
     queries are the newest rows). A row sees the last ``window`` positions up to its own
-    and the first ``sinks``. Returns (O [B, Hq, Nq, d] of o_dtype, LSE fp32 [B, Hq, Nq])."""
+    and the first ``sinks``. Key and value rows below kv_len must be finite, also where no
+    row sees them (padding included). Returns (O [B, Hq, Nq, d] of o_dtype, LSE fp32 [B, Hq, Nq])."""
     bf16 = _is_bf16(o_dtype)
     if scale is None:
         scale = 1.0 if not isinstance(q, torch.Tensor) or q.dim() != 4 else q.shape[3] ** -0.5
