@@ -5,6 +5,9 @@ Thin bindings over the entry points of the same names in ``include/attn.h``: the
 torch tensors, allocate the outputs that are not given (and workspaces), and launch on the
 tensors' device and its current stream (or ``stream``). The marshalling is native
 (``csrc/serving_binding.cpp``): a decode step's kernels take microseconds, and so do calls.
+``stream`` is a torch stream, or a handle as an integer (given tensors then have to live until
+it is done with them); the caller orders it behind the work that makes the inputs. What the
+call allocates comes from that stream's memory, never from what the current one still uses.
 A whole prompt can run through ``attn_window_fwd(q, k, v, window=W, sinks=S)`` on the bf16
 tensors. One decoder layer's step over a batch of requests, of which request b adds
 new_lens[b] <= N tokens, the first at position lens[b]::
